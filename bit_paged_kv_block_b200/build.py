@@ -7,6 +7,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,10 +20,12 @@ ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
           "-prec-div=true", "-ftz=false"]
 # per-file extra flags: the quantizer must not contract its IEEE operations into FMAs
-EXTRA = {"rotate_quantize.cu": ["-fmad=false"]}
+EXTRA = {"rotate_quantize.cu": ["-fmad=false"], "rope_append.cu": ["-fmad=false"]}
 SOURCES = ["rotate_quantize.cu", "paged_decode.cu", "paged_decode_bf16.cu", "prefill_tc.cu",
+           "rope_append.cu", "paged_decode_prefix.cu", "paged_decode_mass.cu", "evict.cu",
            "saw_api.cu", "decode_static.cu"]
-HEADERS = ["saw_device.cuh", "saw_internal.h", "decode_common.cuh"]
+HEADERS = ["saw_device.cuh", "saw_internal.h", "decode_common.cuh", "int4_format.cuh",
+           "quantize_device.cuh"]
 
 
 def _nvcc() -> str:
@@ -49,14 +52,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
-    objs = []
-    for src in SOURCES:
+    def compile_one(src: str) -> str:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
         cmd = [nvcc, *ARCH, *COMMON, *EXTRA.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         subprocess.run(cmd, check=True)
-        objs.append(obj)
+        return obj
+
+    with ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+        objs = list(pool.map(compile_one, SOURCES))
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)

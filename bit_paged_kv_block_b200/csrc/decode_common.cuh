@@ -112,18 +112,17 @@ struct DecodeParams {
     float *lse = nullptr;
     int32_t win_part = 0;
     int32_t win_sink = 0, win_recent = 0;
+    // Decode with accumulated attention weights (INT4 pages): logits of every attended (page,
+    // token, row), fp32 [flat page][16][qrows], and lse[row] as above.
+    float *logits = nullptr;
+    uint16_t *out_bf16 = nullptr;   // bf16 output rows (out unused) of the operators that ask for it
+    // Shared-prefix decode: `batch` sequences; with prefix_seq = batch (else -1) the plan holds the
+    // prefix as sequence batch, of prefix_len tokens in the pages of prefix_table.
+    int32_t batch = 0;
+    int32_t prefix_seq = -1;
+    int32_t prefix_len = 0;
+    const int32_t *prefix_table = nullptr;
 };
-
-// Tokens this launch attends over in a sequence of seq_lens[s] tokens (a negative length is
-// passed through, to be flagged).
-__device__ __forceinline__ int attended_len(const DecodeParams &p, int s)
-{
-    const int L = p.seq_lens[s];
-    if (p.win_part == 0 || L < 0)
-        return L;
-    const int W = p.win_sink + p.win_recent;
-    return p.win_part == 1 ? min(L, W) : max(0, L - W);
-}
 
 // ---- per-sequence tables and the work plan -----------------------------------------------------
 
@@ -142,23 +141,47 @@ struct SeqTables {
     }
 };
 
-// Query tokens of sequence s (decode: 1) and its first query row.  kPrefill: a chunked
-// prefill (q_start given); the decode instantiation has none of the per-row arithmetic.
-template <bool kPrefill>
+// What a launch attends over: a decode (one query token per sequence), a chunked prefill (q_start
+// given), or the shared-prefix decode (paged_decode_prefix.cu), whose plan may hold one more
+// sequence, the prefix (index prefix_seq), that every sequence's query row attends over in full.
+constexpr int kModeDecode = 0;
+constexpr int kModePrefill = 1;
+constexpr int kModePrefix = 2;
+
+// Query tokens of sequence s (decode: 1) and its first query row; the decode instantiation has
+// none of the per-row arithmetic.
+template <int kMode>
 __device__ __forceinline__ int query_tokens(const DecodeParams &p, int s)
 {
-    return kPrefill ? p.q_start[s + 1] - p.q_start[s] : 1;
+    if (kMode == kModePrefix)
+        return s == p.prefix_seq ? p.batch : 1;
+    return kMode == kModePrefill ? p.q_start[s + 1] - p.q_start[s] : 1;
 }
-template <bool kPrefill>
+// Tokens this launch attends over in a sequence of seq_lens[s] tokens (a negative length is
+// passed through, to be flagged).
+template <int kMode>
+__device__ __forceinline__ int attended_len(const DecodeParams &p, int s)
+{
+    if (kMode == kModePrefix && s == p.prefix_seq)
+        return p.prefix_len;
+    const int L = p.seq_lens[s];
+    if (p.win_part == 0 || L < 0)
+        return L;
+    const int W = p.win_sink + p.win_recent;
+    return p.win_part == 1 ? min(L, W) : max(0, L - W);
+}
+template <int kMode>
 __device__ __forceinline__ int64_t query_row0(const DecodeParams &p, int s)
 {
-    return kPrefill ? p.q_start[s] : s;
+    if (kMode == kModePrefix)
+        return s == p.prefix_seq ? 0 : s;
+    return kMode == kModePrefill ? p.q_start[s] : s;
 }
 
 // Fill the tables (every thread of the block takes part).  A sequence with an invalid length
 // or query count (C > L, or C > 0 with L = 0 in prefill) is flagged and gets no segments; a
 // decode sequence of length 0 gets none either (its output row is zeroed).
-template <bool kPrefill>
+template <int kMode>
 __device__ inline void scan_sequences(const DecodeParams &p, const SeqTables &tb,
                                       volatile int64_t *flags, bool report)
 {
@@ -169,10 +192,11 @@ __device__ inline void scan_sequences(const DecodeParams &p, const SeqTables &tb
     int64_t local_pages = 0;
     int32_t local_segs = 0;
     for (int s = s0; s < s1; s++) {
-        const int len = attended_len(p, s);
-        const int c = query_tokens<kPrefill>(p, s);
-        const bool len_ok = len >= 0 && len <= p.max_blocks * kPageSize;
-        const bool q_ok = !kPrefill || (c >= 0 && c <= len);
+        const int len = attended_len<kMode>(p, s);
+        const int c = query_tokens<kMode>(p, s);
+        const bool len_ok = len >= 0 && (len <= p.max_blocks * kPageSize ||
+                                         (kMode == kModePrefix && s == p.prefix_seq));
+        const bool q_ok = kMode != kModePrefill || (c >= 0 && c <= len);
         if (report && !(len_ok && q_ok))
             set_status(p.status, SAW_DEV_BAD_SEQ_LEN);
         const int n = (len_ok && q_ok) ? (len + kPageSize - 1) / kPageSize : 0;
@@ -304,7 +328,7 @@ struct Plan {
 };
 
 // One segment: sequence s, its segment j = kv head h * nb + row block b.
-template <bool kPrefill>
+template <int kMode>
 struct Segment {
     int s, j, h, b;
     int n;          // pages
@@ -322,21 +346,24 @@ struct Segment {
         h = nb == 1 ? j : j / nb;
         b = j - h * nb;
         n = tb.npg[s];
-        c = query_tokens<kPrefill>(p, s);
-        len = attended_len(p, s);
+        c = query_tokens<kMode>(p, s);
+        len = attended_len<kMode>(p, s);
         row0 = kRowsPerBlock * b;
         nrows = min(kRowsPerBlock, c * p.group - row0);
-        qrow0 = query_row0<kPrefill>(p, s);
+        qrow0 = query_row0<kMode>(p, s);
     }
     // query token and head (within the kv head's group) of block row e; a decode has one
     // token, so no division there
     __device__ int row_token(const DecodeParams &p, int e) const
     {
-        return kPrefill ? (row0 + e) / p.group : 0;
+        return kMode != kModeDecode ? (row0 + e) / p.group : 0;
     }
-    // causal limit of block row e (0..7): the last cache token it sees
+    // causal limit of block row e (0..7): the last cache token it sees (every query token sees
+    // the whole of a shared prefix)
     __device__ int limit(const DecodeParams &p, int e) const
     {
+        if (kMode == kModePrefix)
+            return len - 1;
         return len - c + row_token(p, e);
     }
     // q / out element offset of block row e (e < nrows) for head dimension d
@@ -494,6 +521,28 @@ __device__ __forceinline__ void store_partial(float *slot, int lane, const WarpS
     }
 }
 
+// Store this warp's piece as rows: O as [8 rows][D] fp32, then m[8], l[8] (the same slot size).
+// The value dimension of accumulator row (tile 2 c + k, half h) of thread (g, t) is 32 c + 4 g +
+// 2 k + h (the INT4 format's order).
+template <int kTiles>
+__device__ __forceinline__ void store_partial_rows(float *slot, int lane, const WarpState<kTiles> &st)
+{
+    const int g = lane >> 2, t = lane & 3;
+    constexpr int kD = kTiles * 16;
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+        float4 *row = reinterpret_cast<float4 *>(slot + (2 * t + e) * kD) + g;
+#pragma unroll
+        for (int c = 0; c < kTiles / 2; c++)
+            row[8 * c] = make_float4(st.o[2 * c][e], st.o[2 * c][2 + e], st.o[2 * c + 1][e],
+                                     st.o[2 * c + 1][2 + e]);
+        if (g == 0) {
+            slot[8 * kD + 2 * t + e] = st.m[e];
+            slot[8 * kD + 8 + 2 * t + e] = st.l[e];
+        }
+    }
+}
+
 template <int kTiles>
 __device__ __forceinline__ void load_partial(const float *slot, int lane, float bm[2], float bl[2],
                                              float4 (&bo)[kTiles])
@@ -514,7 +563,7 @@ __device__ __forceinline__ void load_partial(const float *slot, int lane, float 
 // (m, l, o) for global segment g; the warps of a block fold disjoint subsets in a fixed order,
 // then warp 0 folds the other warps' results in warp order and writes the output through the
 // page format's finalize step, so the result does not depend on timing.
-template <class Fmt, bool kPrefill, int kMW = kMergeWarps>
+template <class Fmt, int kMode, int kMW = kMergeWarps>
 __global__ void __launch_bounds__(32 * kMW)
     paged_decode_merge_kernel(const DecodeParams p)
 {
@@ -528,7 +577,7 @@ __global__ void __launch_bounds__(32 * kMW)
     volatile int64_t *flags = reinterpret_cast<volatile int64_t *>(smem + merge_smem_flags<kTiles, kMW>());
     float *slots = reinterpret_cast<float *>(smem);
 
-    scan_sequences<kPrefill>(p, tb, flags, false);
+    scan_sequences<kMode>(p, tb, flags, false);
     Plan plan;
     plan.init(tb, p.num_seqs, p.total_warps);
     pdl_wait();   // the decode kernel's partials
@@ -571,7 +620,7 @@ __global__ void __launch_bounds__(32 * kMW)
                 load_partial(slots + (w - 1) * kSlot, lane, bm, bl, bo);
                 merge_into(st.m, st.l, st.o, bm, bl, bo);
             }
-            Segment<kPrefill> sg;
+            Segment<kMode> sg;
             sg.init(p, tb, s, j);
             Fmt::finalize(p, sg, lane, st.o, st.m, st.l);
         }
@@ -627,7 +676,7 @@ inline size_t decode_smem_bytes(int32_t num_seqs, int32_t qrows)
     return 1024 + smem_tables_offset<Fmt>(qrows) + seq_table_bytes(num_seqs);
 }
 
-template <class Fmt, bool kPrefill>
+template <class Fmt, int kMode>
 __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmap, const DecodeParams p)
 {
@@ -641,7 +690,7 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
     volatile int64_t *flags = reinterpret_cast<volatile int64_t *>(smem + smem_flags_offset<Fmt>());
 
     // ---- 1. sequence tables, the plan, zero the output rows that get no segment ----------------
-    scan_sequences<kPrefill>(p, tb, flags, blockIdx.x == 0);
+    scan_sequences<kMode>(p, tb, flags, blockIdx.x == 0);
     // The merge kernel may start its own prologue.  The window part of a windowed decode holds
     // its dependent (the quantized part) back until the cache writes it waits for are complete
     // (below), so that the quantized part can read the cache at once.
@@ -649,10 +698,17 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
         pdl_launch_dependents();
     // (the quantized part of a windowed decode leaves such rows to the window part, which
     // also marks their lse empty)
-    for (int s = blockIdx.x; s < S && p.win_part != 2; s += gridDim.x) {
-        const int c = query_tokens<kPrefill>(p, s);
-        if (tb.nbk[s] == 0 && c > 0 && (!kPrefill || c <= p.seq_lens[s])) {
-            const int64_t row0 = query_row0<kPrefill>(p, s) * p.hq;
+    // (of a shared-prefix decode, every row is written by the merge kernel)
+    for (int s = blockIdx.x; s < S && p.win_part != 2 && kMode != kModePrefix; s += gridDim.x) {
+        const int c = query_tokens<kMode>(p, s);
+        if (tb.nbk[s] == 0 && c > 0 && (kMode != kModePrefill || c <= p.seq_lens[s])) {
+            const int64_t row0 = query_row0<kMode>(p, s) * p.hq;
+            if constexpr (Fmt::kLogits) {
+                uint2 *dst = reinterpret_cast<uint2 *>(p.out_bf16 + row0 * Fmt::kDim);
+                for (int i = tid; i < c * p.hq * Fmt::kDim / 4; i += 32 * Fmt::kWarps)
+                    dst[i] = make_uint2(0u, 0u);
+                continue;
+            }
             float4 *dst = reinterpret_cast<float4 *>(p.out + row0 * Fmt::kDim);
             for (int i = tid; i < c * p.hq * Fmt::kDim / 4; i += 32 * Fmt::kWarps)
                 dst[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -665,7 +721,7 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
     // before it releases the quantized part, and the quantized part completes only after the
     // window part (its merge kernel reads the window part's rows).
     auto pdl_exit = [&]() {
-        if (p.win_part != 0)
+        if (p.win_part != 0 || kMode == kModePrefix)
             pdl_wait();
         if (p.win_part == 1)
             pdl_launch_dependents();
@@ -727,7 +783,10 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
         const int i = static_cast<int>(rel - static_cast<int64_t>(j) * n_s);
         const int nb = tb.nbk[s];
         const int h = nb == 1 ? j : j / nb;
-        int32_t page = p.block_table[static_cast<int64_t>(s) * p.max_blocks + i];
+        const int32_t *table = p.block_table + static_cast<int64_t>(s) * p.max_blocks;
+        if (kMode == kModePrefix && s == p.prefix_seq)
+            table = p.prefix_table;
+        int32_t page = table[i];
         if (page < 0 || page >= p.num_pages) {
             set_status(p.status, SAW_DEV_BAD_PAGE);
             page = 0;
@@ -736,7 +795,7 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
     };
     // queue a segment's raw query rows into the warp's query buffer: one bulk copy per run of
     // rows of the same query token (its heads are contiguous)
-    auto issue_query = [&](const Segment<kPrefill> &sg) {
+    auto issue_query = [&](const Segment<kMode> &sg) {
         if (lane == 0) {
             mbar_arrive_expect_tx(qbar, static_cast<uint32_t>(sg.nrows) * Fmt::kDim * 2);
             for (int e = 0; e < sg.nrows;) {
@@ -752,7 +811,9 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
     // The cache may be written by the kernel this one depends on.  The quantized part of a
     // windowed decode depends on the window part, which released it only after that kernel's
     // writes were complete: it waits only where it needs the window part's rows (finalize).
-    if (p.win_part != 2)
+    // A shared-prefix decode reads nothing that the kernel before it (the prefix part, which
+    // starts after all earlier work) writes.
+    if (p.win_part != 2 && kMode != kModePrefix)
         pdl_wait();
     if (p.win_part == 1)
         pdl_launch_dependents();
@@ -783,7 +844,7 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
     int cs = plan.seq_of_flat(F0);
     int cj = static_cast<int>((F0 - tb.fpre[cs]) / tb.npg[cs]);
     {
-        Segment<kPrefill> sg;
+        Segment<kMode> sg;
         sg.init(p, tb, cs, cj);
         issue_query(sg);
     }
@@ -800,6 +861,8 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
         const int stg = m % kStages;
         const uint32_t phase = (static_cast<uint32_t>(m) / kStages) & 1u;
         const bool ok = !aborted && mbar_wait_bounded(bar0 + 8 * stg, phase, kWaitLimitNs);
+        if constexpr (Fmt::kLogits)
+            qf.logits = p.logits + (F0 + m) * (kPageSize * p.qrows);
         if (__all_sync(0xFFFFFFFFu, ok)) {
             Fmt::template page<decltype(mask_tag)::value>(ring, stg, mask, qf, lane, st);
         } else if (!aborted) {
@@ -820,6 +883,8 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
         const bool ok = !aborted &&
                         mbar_wait_bounded(bar0 + 8 * stg0, (static_cast<uint32_t>(m) / kStages) & 1u, kWaitLimitNs) &&
                         mbar_wait_bounded(bar0 + 8 * stg1, (static_cast<uint32_t>(m + 1) / kStages) & 1u, kWaitLimitNs);
+        if constexpr (Fmt::kLogits)
+            qf.logits = p.logits + (F0 + m) * (kPageSize * p.qrows);
         if (__all_sync(0xFFFFFFFFu, ok)) {
             if constexpr (Fmt::kPairs)
                 Fmt::page2(ring, stg0, stg1, qf, lane, st);
@@ -845,7 +910,7 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
         const int m_end = static_cast<int>((ends_segment ? seg_end : F1) - F0);
         int len, lim[2], first_masked, nrows;
         {
-            Segment<kPrefill> sg;
+            Segment<kMode> sg;
             sg.init(p, tb, cs, cj);
             len = sg.len;
             lim[0] = sg.limit(p, 2 * t4);
@@ -876,7 +941,7 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
                 nj = 0;
             }
             if (!aborted) {
-                Segment<kPrefill> nx;
+                Segment<kMode> nx;
                 nx.init(p, tb, ns, nj);
                 issue_query(nx);
             }
@@ -897,8 +962,15 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
             step(std::true_type(), m, page_mask(len, lim, i0 + m));
 
         Fmt::piece_end(st);
-        if (seg_start >= F0 && ends_segment) {
-            Segment<kPrefill> sg;
+        if constexpr (kMode == kModePrefix) {
+            // every piece goes to its slot; the prefix's pieces as rows, for the merge kernel
+            float *slot = p.partials + (tb.spre[cs] + cj + u) * slot_floats<Fmt::kTiles>();
+            if (cs == p.prefix_seq)
+                store_partial_rows(slot, lane, st);
+            else
+                store_partial(slot, lane, st);
+        } else if (seg_start >= F0 && ends_segment) {
+            Segment<kMode> sg;
             sg.init(p, tb, cs, cj);
             if (p.win_part == 2)
                 pdl_wait();   // the window part's rows and lse
@@ -918,7 +990,7 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
                               kWaitLimitNs / 10);
         mbar_wait_bounded(qbar, qphase, kWaitLimitNs / 10);
     }
-    if (p.win_part == 2)
+    if (p.win_part == 2 || kMode == kModePrefix)
         pdl_wait();   // complete only after the window part (the merge kernel reads its rows)
 }
 

@@ -1,0 +1,205 @@
+// paged_decode_mass.cu -- decode attention over the INT4 paged cache that also accumulates the
+// attention weight every cached token received.
+//
+// out[s, hq] as the decode (paged_decode.cu); and for each cached token t of sequence s and kv head h
+//     mass[page(t)][h][t mod 16] += sum over the G query heads of h of softmax(logits)_t,
+// the quantity an eviction keeps the heaviest tokens by (evict.cu).
+//
+// The weight needs the row's final maximum and sum, which exist only once every piece of its
+// segment is merged.  The decode kernel therefore stores the logits it forms (fp32, 4 bytes per
+// token and query head, [flat page][16][rows] so that a page's store is contiguous), the decode or
+// its merge stores each row's lse = m + log2 l, and a third kernel reads both, forms
+// 2^(logit - lse) and adds the heads' sum to the token's mass.  Reading the stored logits back (16 B
+// per token and kv head at G = 4, from L2 while they fit) costs less than re-reading the token's
+// 68 B of key codes and scales and repeating QK^T.
+//
+// The masses are fp32 states, so the logits are formed to fp32's accuracy: the query enters the
+// tensor cores as fp16 high and low parts (the codes are exact there).
+#include <algorithm>
+
+#include "int4_format.cuh"
+
+namespace saw {
+namespace {
+
+struct MassParams {
+    DecodeParams d;
+    float *mass;             // fp32 [num_pages][Hkv][16]
+    int32_t blocks_per_kv;   // row blocks of a kv head: ceil(G / 8)
+};
+
+constexpr int kMassThreads = 256;
+
+inline size_t mass_smem_bytes(int32_t num_seqs)
+{
+    return 16 * (kMassThreads / 32) + seq_table_bytes(num_seqs);
+}
+
+// One half warp per (sequence, kv head, page), lane = token.  Tokens of one page and kv head are
+// owned by one lane, which sums its heads in a fixed order; the add is a reduction without return,
+// so it is exact-order unless two sequences of the call share a page.
+__global__ void __launch_bounds__(kMassThreads) mass_accumulate_kernel(const MassParams mp)
+{
+    const DecodeParams &p = mp.d;
+    extern __shared__ __align__(16) uint8_t smem[];
+    volatile int64_t *flags = reinterpret_cast<volatile int64_t *>(smem);
+    SeqTables tb;
+    tb.bind(smem + 16 * (kMassThreads / 32), p.num_seqs);
+    scan_sequences<kModeDecode>(p, tb, flags, false);
+    Plan plan;
+    plan.init(tb, p.num_seqs, p.total_warps);
+    pdl_wait();   // logits and lse
+    const int nb = mp.blocks_per_kv, tok = threadIdx.x & 15;
+    const int64_t units = plan.P / nb, step = static_cast<int64_t>(gridDim.x) * (kMassThreads / 16);
+    for (int64_t u = (static_cast<int64_t>(blockIdx.x) * kMassThreads + threadIdx.x) / 16; u < units; u += step) {
+        const int s = plan.seq_of_flat(u * nb);
+        const int n = tb.npg[s];
+        const int rel = static_cast<int>(u - tb.fpre[s] / nb);
+        const int h = rel / n, i = rel - h * n;
+        const int32_t page = p.block_table[static_cast<int64_t>(s) * p.max_blocks + i];
+        if (page < 0 || page >= p.num_pages || kPageSize * i + tok >= p.seq_lens[s])
+            continue;
+        float sum = 0.0f;
+        for (int b = 0; b < nb; b++) {
+            const int rows = min(kRowsPerBlock, p.group - kRowsPerBlock * b);
+            const float *lg = p.logits + ((tb.fpre[s] + static_cast<int64_t>(h * nb + b) * n + i) * kPageSize + tok) *
+                                             p.qrows;
+            const float *lse = p.lse + static_cast<int64_t>(s) * p.hq + h * p.group + kRowsPerBlock * b;
+            for (int c = 0; c < rows; c++)
+                sum += ex2_approx(lg[c] - lse[c]);
+        }
+        atomicAdd(mp.mass + (static_cast<int64_t>(page) * p.hkv + h) * kPageSize + tok, sum);
+    }
+}
+
+template <bool kRotate, int kD>
+using MassFormat = Int4Format<kRotate, kD, kRoleMass>;
+
+template <int kD>
+cudaError_t mass_shape(size_t smem, size_t merge_smem, LaunchShape &out)
+{
+    static ShapeCache shapes;
+    static const void *const decode_kernels[kShapeVariants] = {
+        reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<true, kD>, kModeDecode>),
+        reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<false, kD>, kModeDecode>),
+        reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<true, kD>, kModeDecode>),
+        reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<false, kD>, kModeDecode>)};
+    static const void *const merge_kernels[kShapeVariants] = {
+        reinterpret_cast<const void *>(paged_decode_merge_kernel<MassFormat<true, kD>, kModeDecode>),
+        reinterpret_cast<const void *>(paged_decode_merge_kernel<MassFormat<false, kD>, kModeDecode>),
+        reinterpret_cast<const void *>(paged_decode_merge_kernel<MassFormat<true, kD>, kModeDecode>),
+        reinterpret_cast<const void *>(paged_decode_merge_kernel<MassFormat<false, kD>, kModeDecode>)};
+    return decode::launch_shape(shapes, decode_kernels, merge_kernels, 32 * MassFormat<true, kD>::kWarps,
+                                smem, merge_smem, out);
+}
+
+// Workspace: the split-K slots, lse [S][Hq], then the logits of every page the block table can hold.
+struct MassWorkspace {
+    size_t lse, logits, total;
+};
+
+template <int kD>
+cudaError_t mass_workspace(int32_t hkv, int32_t hq, int32_t num_seqs, int32_t max_blocks, LaunchShape &ls,
+                           MassWorkspace &w)
+{
+    using Fmt = MassFormat<true, kD>;
+    const int32_t qrows = query_rows(hkv, hq, false);
+    const cudaError_t e = mass_shape<kD>(decode_smem_bytes<Fmt>(num_seqs, qrows),
+                                         merge_smem_bytes<Fmt::kTiles>(num_seqs), ls);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t segments = max_segments(hkv, hq, num_seqs, 0, false);
+    auto round = [](size_t n) { return (n + 255) / 256 * 256; };
+    w.lse = round(workspace_bytes_for<Fmt::kTiles>(static_cast<size_t>(ls.sms) * ls.occ * Fmt::kWarps, segments));
+    w.logits = w.lse + round(static_cast<size_t>(num_seqs) * hq * sizeof(float));
+    w.total = w.logits + static_cast<size_t>(segments) * max_blocks * kPageSize * qrows * sizeof(float);
+    return cudaSuccess;
+}
+
+template <bool kRotate, int kD>
+cudaError_t launch(const DecodeArgs &a, float *mass, cudaStream_t stream, bool programmatic)
+{
+    using Fmt = MassFormat<kRotate, kD>;
+    const CUtensorMap *map = code_tensor_map<kD>(a.kv_pages, a.num_pages * a.num_kv_heads * 32);
+    if (map == nullptr)
+        return cudaErrorInvalidValue;
+    LaunchShape ls;
+    MassWorkspace w;
+    cudaError_t e = mass_workspace<kD>(a.num_kv_heads, a.num_q_heads, a.num_seqs, a.max_blocks, ls, w);
+    if (e != cudaSuccess)
+        return e;
+    MassParams mp;
+    DecodeParams &p = mp.d;
+    fill_decode_params<kD>(a, p);
+    p.qrows = query_rows(a.num_kv_heads, a.num_q_heads, false);
+    p.max_segments = max_segments(a.num_kv_heads, a.num_q_heads, a.num_seqs, 0, false);
+    p.total_warps = ls.sms * ls.occ * Fmt::kWarps;
+    p.lse = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + w.lse);
+    p.logits = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + w.logits);
+    mp.mass = mass;
+    mp.blocks_per_kv = (p.group + kRowsPerBlock - 1) / kRowsPerBlock;
+
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ls.sms * ls.occ));
+    cfg.blockDim = dim3(32 * Fmt::kWarps);
+    cfg.dynamicSmemBytes = decode_smem_bytes<Fmt>(a.num_seqs, p.qrows);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = programmatic ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<Fmt, kModeDecode>, *map, p);
+    if (e != cudaSuccess)
+        return e;
+
+    cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(p.max_segments, 8 * ls.sms))));
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = merge_smem_bytes<Fmt::kTiles>(a.num_seqs);
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_decode_merge_kernel<Fmt, kModeDecode>, p);
+    if (e != cudaSuccess)
+        return e;
+
+    cfg.gridDim = dim3(static_cast<unsigned>(4 * ls.sms));
+    cfg.blockDim = dim3(kMassThreads);
+    cfg.dynamicSmemBytes = mass_smem_bytes(a.num_seqs);
+    e = cudaLaunchKernelEx(&cfg, mass_accumulate_kernel, mp);
+    if (e != cudaSuccess)
+        return e;
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t decode_mass_workspace_bytes(int32_t num_kv_heads, int32_t num_q_heads, int32_t num_seqs,
+                                   int32_t max_blocks, int32_t head_dim)
+{
+    LaunchShape ls;
+    MassWorkspace w;
+    const cudaError_t e =
+        head_dim == 64    ? mass_workspace<64>(num_kv_heads, num_q_heads, num_seqs, max_blocks, ls, w)
+        : head_dim == 128 ? mass_workspace<128>(num_kv_heads, num_q_heads, num_seqs, max_blocks, ls, w)
+        : head_dim == 256 ? mass_workspace<256>(num_kv_heads, num_q_heads, num_seqs, max_blocks, ls, w)
+                          : cudaErrorInvalidValue;
+    return e == cudaSuccess ? w.total : 0;
+}
+
+cudaError_t launch_paged_decode_mass(const DecodeArgs &a, float *mass, cudaStream_t stream, bool programmatic)
+{
+    switch (a.head_dim) {
+    case 64:
+        return a.rotate ? launch<true, 64>(a, mass, stream, programmatic)
+                        : launch<false, 64>(a, mass, stream, programmatic);
+    case 128:
+        return a.rotate ? launch<true, 128>(a, mass, stream, programmatic)
+                        : launch<false, 128>(a, mass, stream, programmatic);
+    case 256:
+        return a.rotate ? launch<true, 256>(a, mass, stream, programmatic)
+                        : launch<false, 256>(a, mass, stream, programmatic);
+    default:
+        return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace saw

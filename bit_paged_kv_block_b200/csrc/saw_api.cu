@@ -765,4 +765,497 @@ int saw_decode_step_window(const saw_cache_desc *cache, const saw_window_cache *
                               workspace_bytes, dev_status, st, true);
 }
 
+// ---- rotary positions ------------------------------------------------------------------------
+
+// Frequencies of a rotary embedding in turns per position, and its amplitude (saw.h); false for
+// scaling parameters out of range.
+static bool rope_turns(const saw_rope_scaling &sc, int32_t rotary_dim, double *turns, double &amplitude)
+{
+    const double kTwoPi = 6.283185307179586476925286766559;
+    const double R = rotary_dim;
+    auto finite = [](double x) { return std::isfinite(x); };
+    if (!finite(sc.base) || sc.base <= 1.0 || !finite(sc.amplitude) || sc.amplitude < 0.0)
+        return false;
+    if (sc.kind != SAW_ROPE_PLAIN && (!finite(sc.factor) || sc.factor < 1.0))
+        return false;
+    double base = sc.base, lo = 0.0, hi = 0.0;
+    amplitude = sc.amplitude != 0.0 ? sc.amplitude : 1.0;
+    switch (sc.kind) {
+    case SAW_ROPE_PLAIN:
+    case SAW_ROPE_LINEAR:
+        break;
+    case SAW_ROPE_NTK:
+        base *= std::pow(sc.factor, R / (R - 2.0));
+        break;
+    case SAW_ROPE_BANDED:
+        if (!finite(sc.original_positions) || sc.original_positions <= 0.0 || !finite(sc.low) ||
+            !finite(sc.high) || sc.low >= sc.high)
+            return false;
+        break;
+    case SAW_ROPE_YARN: {
+        if (!finite(sc.original_positions) || sc.original_positions <= 0.0 || !finite(sc.fast) ||
+            !finite(sc.slow) || sc.fast <= 0.0 || sc.slow <= 0.0)
+            return false;
+        auto at = [&](double b) { return R * std::log(sc.original_positions / (kTwoPi * b)) / (2.0 * std::log(base)); };
+        lo = std::max(0.0, std::floor(at(sc.fast)));
+        hi = std::min(R - 1.0, std::ceil(at(sc.slow)));
+        if (sc.amplitude == 0.0)
+            amplitude = 0.1 * std::log(sc.factor) + 1.0;
+        break;
+    }
+    default:
+        return false;
+    }
+    for (int i = 0; i < rotary_dim / 2; i++) {
+        double f = std::pow(base, -2.0 * i / R);
+        if (sc.kind == SAW_ROPE_LINEAR) {
+            f /= sc.factor;
+        } else if (sc.kind == SAW_ROPE_BANDED) {
+            const double r = sc.original_positions * f / kTwoPi;
+            const double t = std::min(1.0, std::max(0.0, (r - sc.low) / (sc.high - sc.low)));
+            f *= (1.0 - t) / sc.factor + t;
+        } else if (sc.kind == SAW_ROPE_YARN) {
+            const double t = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
+            f *= t / sc.factor + (1.0 - t);
+        }
+        turns[i] = f / kTwoPi;
+    }
+    return true;
+}
+
+int saw_rope_table(float *table, int64_t first_position, int64_t num_positions, int32_t rotary_dim,
+                   const saw_rope_scaling *scaling, void *stream)
+{
+    if (scaling == nullptr || first_position < 0 || num_positions < 0 || rotary_dim <= 0)
+        return SAW_ERR_INVALID_ARGUMENT;
+    const int64_t most = int64_t(1) << 31;
+    if (first_position > most || num_positions > most - first_position)
+        return SAW_ERR_INVALID_ARGUMENT;
+    if (rotary_dim % 16 != 0 || rotary_dim > 256)
+        return SAW_ERR_UNSUPPORTED;
+    saw::RopeTableArgs a;
+    if (!rope_turns(*scaling, rotary_dim, a.turns, a.amplitude))
+        return SAW_ERR_INVALID_ARGUMENT;
+    if (num_positions == 0)
+        return SAW_OK;
+    if (table == nullptr || !aligned(table, 16))
+        return SAW_ERR_INVALID_ARGUMENT;
+    a.table = table;
+    a.first_position = first_position;
+    a.num_positions = num_positions;
+    a.rotary_dim = rotary_dim;
+    return saw::launch_rope_table(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
+}
+
+static int check_rope(const saw_cache_desc *cache, const saw_rope *rope)
+{
+    if (rope == nullptr || rope->num_positions < 0 || rope->rotary_dim <= 0 ||
+        (rope->interleaved != 0 && rope->interleaved != 1))
+        return SAW_ERR_INVALID_ARGUMENT;
+    if (rope->rotary_dim % 16 != 0 || rope->rotary_dim > cache->head_dim)
+        return SAW_ERR_UNSUPPORTED;
+    if (rope->num_positions > (int64_t(1) << 31))
+        return SAW_ERR_INVALID_ARGUMENT;
+    return SAW_OK;
+}
+
+// A token stride of `heads` head vectors: 0 (contiguous), or at least their elements and a multiple
+// of 8.
+static bool stride_ok(int64_t stride, int64_t heads, int64_t head_dim)
+{
+    return stride == 0 || (stride >= heads * head_dim && stride % 8 == 0 && stride <= (int64_t(1) << 36));
+}
+
+static int check_rope_append(const saw_cache_desc *cache, const saw_rope *rope, int32_t num_q_heads,
+                             const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                             const void *v, int64_t v_stride, const int64_t *positions,
+                             const int64_t *slot_mapping, int64_t num_tokens, const void *q_out,
+                             const uint8_t *kv_pages, const void *scales, const float *mass)
+{
+    int rc = check_cache(cache);
+    if (rc != SAW_OK)
+        return rc;
+    rc = check_rope(cache, rope);
+    if (rc != SAW_OK)
+        return rc;
+    rc = check_append(cache, k, v, slot_mapping, num_tokens, kv_pages, scales);
+    if (rc != SAW_OK)
+        return rc;
+    if (num_q_heads < 0 || !stride_ok(q_stride, num_q_heads, cache->head_dim) ||
+        !stride_ok(k_stride, cache->num_kv_heads, cache->head_dim) ||
+        !stride_ok(v_stride, cache->num_kv_heads, cache->head_dim))
+        return SAW_ERR_INVALID_ARGUMENT;
+    const int64_t row = int64_t(cache->num_kv_heads) * cache->head_dim;
+    const bool strided = (k_stride != 0 && k_stride != row) || (v_stride != 0 && v_stride != row);
+    const int64_t tile_vecs = 1024 / cache->head_dim;   // vectors of a 16-row box
+    if (strided && cache->num_kv_heads % tile_vecs != 0 && tile_vecs % cache->num_kv_heads != 0)
+        return SAW_ERR_UNSUPPORTED;
+    if (num_tokens == 0)
+        return SAW_OK;
+    // the kernel counts 64-element rows in 32 bits
+    if (num_tokens > (int64_t(1) << 29) / (int64_t(cache->num_kv_heads) * (cache->head_dim / 64)) ||
+        num_tokens > INT64_MAX / (std::max<int64_t>(1, num_q_heads) * cache->head_dim * 2))
+        return SAW_ERR_UNSUPPORTED;
+    if (positions == nullptr || !aligned(positions, 8) || !aligned(mass, 16))
+        return SAW_ERR_INVALID_ARGUMENT;
+    if (rope->table == nullptr || !aligned(rope->table, 16) || rope->num_positions == 0)
+        return SAW_ERR_INVALID_ARGUMENT;
+    if (num_q_heads > 0 && (q == nullptr || q_out == nullptr || !aligned(q, 16) || !aligned(q_out, 16)))
+        return SAW_ERR_INVALID_ARGUMENT;
+    if (q == q_out && num_q_heads > 0 && q_stride != 0 && q_stride != int64_t(num_q_heads) * cache->head_dim)
+        return SAW_ERR_INVALID_ARGUMENT;   // in place only on contiguous rows
+    return SAW_OK;
+}
+
+static int rope_append_impl(const saw_cache_desc *cache, const saw_rope *rope, int32_t num_q_heads,
+                            const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                            const void *v, int64_t v_stride, const int64_t *positions,
+                            const int64_t *slot_mapping, int64_t num_tokens, void *q_out,
+                            uint8_t *kv_pages, void *scales, float *mass, uint32_t *dev_status,
+                            void *stream, bool rotate)
+{
+    const int64_t row = int64_t(cache->num_kv_heads) * cache->head_dim;
+    k_stride = k_stride != 0 ? k_stride : row;
+    v_stride = v_stride != 0 ? v_stride : row;
+    const bool strided = k_stride != row || v_stride != row;
+    saw::RopeAppendArgs a;
+    a.kv = append_args(cache, k, v, slot_mapping, num_tokens, kv_pages, scales, dev_status, rotate);
+    a.kv.k_stride = strided ? k_stride : 0;
+    a.kv.v_stride = strided ? v_stride : 0;
+    a.q = q;
+    a.q_out = q_out;
+    a.q_stride = q_stride;
+    a.num_q_heads = num_q_heads;
+    a.positions = positions;
+    a.table = rope->table;
+    a.num_positions = rope->num_positions;
+    a.rotary_dim = rope->rotary_dim;
+    a.interleaved = rope->interleaved != 0;
+    a.mass = mass;
+    return saw::launch_rope_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
+}
+
+int saw_rope_rotate_quantize_paged(const saw_cache_desc *cache, const saw_rope *rope,
+                                   int32_t num_q_heads, const void *q, int64_t q_stride,
+                                   const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                   const int64_t *positions, const int64_t *slot_mapping,
+                                   int64_t num_tokens, void *q_out, uint8_t *kv_pages, void *scales,
+                                   float *mass, uint32_t *dev_status, void *stream)
+{
+    const int rc = check_rope_append(cache, rope, num_q_heads, q, q_stride, k, k_stride, v, v_stride,
+                                     positions, slot_mapping, num_tokens, q_out, kv_pages, scales, mass);
+    if (rc != SAW_OK || num_tokens == 0)
+        return rc;
+    return rope_append_impl(cache, rope, num_q_heads, q, q_stride, k, k_stride, v, v_stride, positions,
+                            slot_mapping, num_tokens, q_out, kv_pages, scales, mass, dev_status, stream, true);
+}
+
+int saw_rope_quantize_paged_plain(const saw_cache_desc *cache, const saw_rope *rope,
+                                  int32_t num_q_heads, const void *q, int64_t q_stride,
+                                  const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                  const int64_t *positions, const int64_t *slot_mapping,
+                                  int64_t num_tokens, void *q_out, uint8_t *kv_pages, void *scales,
+                                  float *mass, uint32_t *dev_status, void *stream)
+{
+    const int rc = check_rope_append(cache, rope, num_q_heads, q, q_stride, k, k_stride, v, v_stride,
+                                     positions, slot_mapping, num_tokens, q_out, kv_pages, scales, mass);
+    if (rc != SAW_OK || num_tokens == 0)
+        return rc;
+    return rope_append_impl(cache, rope, num_q_heads, q, q_stride, k, k_stride, v, v_stride, positions,
+                            slot_mapping, num_tokens, q_out, kv_pages, scales, mass, dev_status, stream, false);
+}
+
+// ---- shared-prefix decode, accumulated weights, eviction ----------------------------------------
+
+// The checks of a decode that writes bf16 rows, up to its workspace (`need` bytes; 0: a CUDA error).
+static int check_decode_bf16_out(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
+                                 const uint8_t *kv_pages, const void *scales, const int32_t *block_table,
+                                 int32_t max_blocks, const int32_t *seq_lens, int32_t num_seqs,
+                                 float sm_scale, const void *out)
+{
+    int rc = check_cache(cache);
+    if (rc != SAW_OK)
+        return rc;
+    if (num_q_heads <= 0 || num_seqs < 0 || num_q_heads % cache->num_kv_heads != 0)
+        return SAW_ERR_INVALID_ARGUMENT;
+    if (num_q_heads / cache->num_kv_heads > 16)
+        return SAW_ERR_UNSUPPORTED;
+    if (!std::isfinite(sm_scale))
+        return SAW_ERR_INVALID_ARGUMENT;
+    if (num_seqs == 0)
+        return SAW_OK;
+    if (!q || !kv_pages || !scales || !block_table || !seq_lens || !out || max_blocks <= 0 ||
+        cache->num_pages == 0 || int64_t(max_blocks) * 16 > INT32_MAX)
+        return SAW_ERR_INVALID_ARGUMENT;
+    if (!aligned(q, 16) || !aligned(kv_pages, 16) || !aligned(scales, 16) || !aligned(out, 16) ||
+        !aligned(block_table, 4) || !aligned(seq_lens, 4))
+        return SAW_ERR_INVALID_ARGUMENT;
+    // query rows (num_seqs * num_q_heads) are counted in 32 bits
+    if (int64_t(num_seqs) * num_q_heads > (int64_t(1) << 30))
+        return SAW_ERR_UNSUPPORTED;
+    return SAW_OK;
+}
+
+static int check_workspace(size_t need, const void *workspace, size_t workspace_bytes)
+{
+    if (need == 0)
+        return SAW_ERR_CUDA;
+    return workspace != nullptr && workspace_bytes >= need && aligned(workspace, 256) ? SAW_OK
+                                                                                     : SAW_ERR_WORKSPACE;
+}
+
+// Whether a decode of these sizes is supported (for the workspace sizes).
+static bool decode_sizes_ok(const saw_cache_desc *cache, int32_t num_q_heads, int32_t num_seqs)
+{
+    return check_cache(cache) == SAW_OK && num_q_heads > 0 && num_seqs >= 0 &&
+           num_q_heads % cache->num_kv_heads == 0 && num_q_heads / cache->num_kv_heads <= 16 &&
+           int64_t(num_seqs) * num_q_heads <= (int64_t(1) << 30);
+}
+
+size_t saw_paged_decode_prefix_workspace_bytes(const saw_cache_desc *cache, int32_t num_q_heads,
+                                               int32_t num_seqs, int32_t prefix_len)
+{
+    if (!decode_sizes_ok(cache, num_q_heads, num_seqs) || prefix_len < 0)
+        return 0;
+    return saw::decode_prefix_workspace_bytes(cache->num_kv_heads, num_q_heads, num_seqs, prefix_len,
+                                              cache->head_dim);
+}
+
+static int decode_prefix_impl(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
+                              const uint8_t *kv_pages, const void *scales, const int32_t *prefix_table,
+                              int32_t prefix_len, const int32_t *block_table, int32_t max_blocks_per_seq,
+                              const int32_t *seq_lens, int32_t num_seqs, float sm_scale, void *out,
+                              void *workspace, size_t workspace_bytes, uint32_t *dev_status, void *stream,
+                              bool rotate)
+{
+    int rc = check_decode_bf16_out(cache, num_q_heads, q, kv_pages, scales, block_table, max_blocks_per_seq,
+                                   seq_lens, num_seqs, sm_scale, out);
+    if (rc != SAW_OK)
+        return rc;
+    if (prefix_len < 0 || prefix_len > INT32_MAX - 16)
+        return SAW_ERR_INVALID_ARGUMENT;
+    if (num_seqs == 0)
+        return SAW_OK;
+    if (prefix_len > 0 && (prefix_table == nullptr || !aligned(prefix_table, 4)))
+        return SAW_ERR_INVALID_ARGUMENT;
+    rc = check_workspace(saw::decode_prefix_workspace_bytes(cache->num_kv_heads, num_q_heads, num_seqs,
+                                                            prefix_len, cache->head_dim),
+                         workspace, workspace_bytes);
+    if (rc != SAW_OK)
+        return rc;
+    saw::DecodeArgs a = decode_args(cache, num_q_heads, q, kv_pages, scales, block_table, max_blocks_per_seq,
+                                    seq_lens, num_seqs, sm_scale, nullptr, workspace, workspace_bytes,
+                                    dev_status);
+    a.out_bf16 = out;
+    a.rotate = rotate;
+    return saw::launch_paged_decode_prefix(a, prefix_table, prefix_len, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? SAW_OK
+               : SAW_ERR_CUDA;
+}
+
+int saw_paged_decode_attn_prefix(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
+                                 const uint8_t *kv_pages, const void *scales,
+                                 const int32_t *prefix_table, int32_t prefix_len,
+                                 const int32_t *block_table, int32_t max_blocks_per_seq,
+                                 const int32_t *seq_lens, int32_t num_seqs, float sm_scale, void *out,
+                                 void *workspace, size_t workspace_bytes, uint32_t *dev_status,
+                                 void *stream)
+{
+    return decode_prefix_impl(cache, num_q_heads, q, kv_pages, scales, prefix_table, prefix_len, block_table,
+                              max_blocks_per_seq, seq_lens, num_seqs, sm_scale, out, workspace,
+                              workspace_bytes, dev_status, stream, true);
+}
+
+int saw_paged_decode_attn_prefix_plain(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
+                                       const uint8_t *kv_pages, const void *scales,
+                                       const int32_t *prefix_table, int32_t prefix_len,
+                                       const int32_t *block_table, int32_t max_blocks_per_seq,
+                                       const int32_t *seq_lens, int32_t num_seqs, float sm_scale,
+                                       void *out, void *workspace, size_t workspace_bytes,
+                                       uint32_t *dev_status, void *stream)
+{
+    return decode_prefix_impl(cache, num_q_heads, q, kv_pages, scales, prefix_table, prefix_len, block_table,
+                              max_blocks_per_seq, seq_lens, num_seqs, sm_scale, out, workspace,
+                              workspace_bytes, dev_status, stream, false);
+}
+
+size_t saw_paged_decode_mass_workspace_bytes(const saw_cache_desc *cache, int32_t num_q_heads,
+                                             int32_t num_seqs, int32_t max_blocks_per_seq)
+{
+    if (!decode_sizes_ok(cache, num_q_heads, num_seqs) || max_blocks_per_seq <= 0 ||
+        int64_t(max_blocks_per_seq) * 16 > INT32_MAX)
+        return 0;
+    return saw::decode_mass_workspace_bytes(cache->num_kv_heads, num_q_heads, num_seqs, max_blocks_per_seq,
+                                            cache->head_dim);
+}
+
+static int check_decode_mass(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
+                             const uint8_t *kv_pages, const void *scales, const float *mass,
+                             const int32_t *block_table, int32_t max_blocks_per_seq,
+                             const int32_t *seq_lens, int32_t num_seqs, float sm_scale, const void *out,
+                             const void *workspace, size_t workspace_bytes)
+{
+    const int rc = check_decode_bf16_out(cache, num_q_heads, q, kv_pages, scales, block_table,
+                                         max_blocks_per_seq, seq_lens, num_seqs, sm_scale, out);
+    if (rc != SAW_OK || num_seqs == 0)
+        return rc;
+    if (mass == nullptr || !aligned(mass, 16))
+        return SAW_ERR_INVALID_ARGUMENT;
+    return check_workspace(saw::decode_mass_workspace_bytes(cache->num_kv_heads, num_q_heads, num_seqs,
+                                                            max_blocks_per_seq, cache->head_dim),
+                           workspace, workspace_bytes);
+}
+
+static int decode_mass_impl(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
+                            const uint8_t *kv_pages, const void *scales, float *mass,
+                            const int32_t *block_table, int32_t max_blocks_per_seq,
+                            const int32_t *seq_lens, int32_t num_seqs, float sm_scale, void *out,
+                            void *workspace, size_t workspace_bytes, uint32_t *dev_status, void *stream,
+                            bool rotate, bool programmatic)
+{
+    saw::DecodeArgs a = decode_args(cache, num_q_heads, q, kv_pages, scales, block_table, max_blocks_per_seq,
+                                    seq_lens, num_seqs, sm_scale, nullptr, workspace, workspace_bytes,
+                                    dev_status);
+    a.out_bf16 = out;
+    a.rotate = rotate;
+    return saw::launch_paged_decode_mass(a, mass, static_cast<cudaStream_t>(stream), programmatic) == cudaSuccess
+               ? SAW_OK
+               : SAW_ERR_CUDA;
+}
+
+int saw_paged_decode_attn_mass(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
+                               const uint8_t *kv_pages, const void *scales, float *mass,
+                               const int32_t *block_table, int32_t max_blocks_per_seq,
+                               const int32_t *seq_lens, int32_t num_seqs, float sm_scale, void *out,
+                               void *workspace, size_t workspace_bytes, uint32_t *dev_status,
+                               void *stream)
+{
+    const int rc = check_decode_mass(cache, num_q_heads, q, kv_pages, scales, mass, block_table,
+                                     max_blocks_per_seq, seq_lens, num_seqs, sm_scale, out, workspace,
+                                     workspace_bytes);
+    if (rc != SAW_OK || num_seqs == 0)
+        return rc;
+    return decode_mass_impl(cache, num_q_heads, q, kv_pages, scales, mass, block_table, max_blocks_per_seq,
+                            seq_lens, num_seqs, sm_scale, out, workspace, workspace_bytes, dev_status, stream,
+                            true, false);
+}
+
+int saw_paged_decode_attn_mass_plain(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
+                                     const uint8_t *kv_pages, const void *scales, float *mass,
+                                     const int32_t *block_table, int32_t max_blocks_per_seq,
+                                     const int32_t *seq_lens, int32_t num_seqs, float sm_scale,
+                                     void *out, void *workspace, size_t workspace_bytes,
+                                     uint32_t *dev_status, void *stream)
+{
+    const int rc = check_decode_mass(cache, num_q_heads, q, kv_pages, scales, mass, block_table,
+                                     max_blocks_per_seq, seq_lens, num_seqs, sm_scale, out, workspace,
+                                     workspace_bytes);
+    if (rc != SAW_OK || num_seqs == 0)
+        return rc;
+    return decode_mass_impl(cache, num_q_heads, q, kv_pages, scales, mass, block_table, max_blocks_per_seq,
+                            seq_lens, num_seqs, sm_scale, out, workspace, workspace_bytes, dev_status, stream,
+                            false, false);
+}
+
+int saw_evict_paged(const saw_cache_desc *cache, uint8_t *kv_pages, void *scales, float *mass,
+                    const int32_t *block_table, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                    int32_t num_seqs, const int32_t *new_table, int32_t new_blocks,
+                    int32_t *new_lens, int32_t *kept, int32_t keep, int32_t sink, int32_t recent,
+                    uint32_t *dev_status, void *stream)
+{
+    int rc = check_cache(cache);
+    if (rc != SAW_OK)
+        return rc;
+    if (num_seqs < 0 || keep < 1 || sink < 0 || recent < 0 || int64_t(sink) + recent > keep)
+        return SAW_ERR_INVALID_ARGUMENT;
+    if (num_seqs == 0)
+        return SAW_OK;
+    if (!kv_pages || !scales || !mass || !block_table || !seq_lens || !new_table || !new_lens || !kept ||
+        max_blocks_per_seq <= 0 || new_blocks <= 0 || cache->num_pages == 0 ||
+        int64_t(max_blocks_per_seq) * 16 > INT32_MAX || int64_t(new_blocks) * 16 > INT32_MAX)
+        return SAW_ERR_INVALID_ARGUMENT;
+    if (!aligned(kv_pages, 16) || !aligned(scales, 16) || !aligned(mass, 16) || !aligned(block_table, 4) ||
+        !aligned(seq_lens, 4) || !aligned(new_table, 4) || !aligned(new_lens, 4) || !aligned(kept, 4))
+        return SAW_ERR_INVALID_ARGUMENT;
+    if (new_lens == seq_lens)
+        return SAW_ERR_INVALID_ARGUMENT;
+    // one CTA per (sequence, kv head)
+    if (int64_t(num_seqs) * cache->num_kv_heads > INT32_MAX)
+        return SAW_ERR_UNSUPPORTED;
+    saw::EvictArgs a;
+    a.kv_pages = kv_pages;
+    a.scales = scales;
+    a.mass = mass;
+    a.num_kv_heads = cache->num_kv_heads;
+    a.head_dim = cache->head_dim;
+    a.num_pages = cache->num_pages;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks_per_seq;
+    a.seq_lens = seq_lens;
+    a.num_seqs = num_seqs;
+    a.new_table = new_table;
+    a.new_blocks = new_blocks;
+    a.new_lens = new_lens;
+    a.kept = kept;
+    a.keep = keep;
+    a.sink = sink;
+    a.recent = recent;
+    a.status = dev_status;
+    return saw::launch_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
+}
+
+int saw_decode_step_rope(const saw_cache_desc *cache, const saw_rope *rope, int32_t num_q_heads,
+                         const void *q, const void *k_new, const void *v_new,
+                         const int64_t *positions, const int64_t *slot_mapping, void *q_rot,
+                         uint8_t *kv_pages, void *scales, const int32_t *block_table,
+                         int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t num_seqs,
+                         float sm_scale, float *out, void *workspace, size_t workspace_bytes,
+                         uint32_t *dev_status, void *stream)
+{
+    int rc = check_rope_append(cache, rope, num_q_heads, q, 0, k_new, 0, v_new, 0, positions, slot_mapping,
+                               num_seqs, q_rot, kv_pages, scales, nullptr);
+    if (rc != SAW_OK)
+        return rc;
+    rc = check_decode(cache, num_q_heads, q_rot, kv_pages, scales, block_table, max_blocks_per_seq,
+                      seq_lens, num_seqs, sm_scale, out, workspace, workspace_bytes);
+    if (rc != SAW_OK || num_seqs == 0)
+        return rc;
+    rc = rope_append_impl(cache, rope, num_q_heads, q, 0, k_new, 0, v_new, 0, positions, slot_mapping, num_seqs,
+                          q_rot, kv_pages, scales, nullptr, dev_status, stream, true);
+    if (rc != SAW_OK)
+        return rc;
+    const saw::DecodeArgs d = decode_args(cache, num_q_heads, q_rot, kv_pages, scales, block_table,
+                                          max_blocks_per_seq, seq_lens, num_seqs, sm_scale, out, workspace,
+                                          workspace_bytes, dev_status);
+    return saw::launch_paged_decode(d, static_cast<cudaStream_t>(stream), true) == cudaSuccess ? SAW_OK
+                                                                                               : SAW_ERR_CUDA;
+}
+
+int saw_decode_step_rope_mass(const saw_cache_desc *cache, const saw_rope *rope, int32_t num_q_heads,
+                              const void *q, const void *k_new, const void *v_new,
+                              const int64_t *positions, const int64_t *slot_mapping, void *q_rot,
+                              uint8_t *kv_pages, void *scales, float *mass,
+                              const int32_t *block_table, int32_t max_blocks_per_seq,
+                              const int32_t *seq_lens, int32_t num_seqs, float sm_scale, void *out,
+                              void *workspace, size_t workspace_bytes, uint32_t *dev_status,
+                              void *stream)
+{
+    int rc = check_rope_append(cache, rope, num_q_heads, q, 0, k_new, 0, v_new, 0, positions, slot_mapping,
+                               num_seqs, q_rot, kv_pages, scales, mass);
+    if (rc != SAW_OK)
+        return rc;
+    rc = check_decode_mass(cache, num_q_heads, q_rot, kv_pages, scales, mass, block_table, max_blocks_per_seq,
+                           seq_lens, num_seqs, sm_scale, out, workspace, workspace_bytes);
+    if (rc != SAW_OK || num_seqs == 0)
+        return rc;
+    rc = rope_append_impl(cache, rope, num_q_heads, q, 0, k_new, 0, v_new, 0, positions, slot_mapping, num_seqs,
+                          q_rot, kv_pages, scales, mass, dev_status, stream, true);
+    if (rc != SAW_OK)
+        return rc;
+    return decode_mass_impl(cache, num_q_heads, q_rot, kv_pages, scales, mass, block_table, max_blocks_per_seq,
+                            seq_lens, num_seqs, sm_scale, out, workspace, workspace_bytes, dev_status, stream,
+                            true, true);
+}
+
 }  // extern "C"

@@ -266,6 +266,13 @@ __device__ __forceinline__ uint32_t half2_as_u32(__half2 h)
 {
     return *reinterpret_cast<uint32_t *>(&h);
 }
+// (lo, hi) rounded to bf16, packed
+__device__ __forceinline__ uint32_t bf16x2_as_u32(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ __half2 u32_as_half2(uint32_t u)
 {
     return *reinterpret_cast<__half2 *>(&u);

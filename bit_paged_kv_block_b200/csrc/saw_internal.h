@@ -64,6 +64,7 @@ struct DecodeArgs {
     int32_t win_part = 0;
     int32_t win_sink = 0, win_recent = 0;
     float *lse = nullptr;        // [S][Hq] log2 softmax denominators of the window part
+    void *out_bf16 = nullptr;    // bf16 [S][Hq][D]: the output of the operators below that write bf16
 };
 
 struct AppendBf16Args {
@@ -125,5 +126,63 @@ cudaError_t launch_window_append(const WindowAppendArgs &a, cudaStream_t stream)
 size_t decode_bf16_workspace_bytes(int32_t num_kv_heads, int32_t num_q_heads, int32_t num_seqs,
                                    int64_t total_q = -1);
 cudaError_t launch_paged_decode_bf16(const DecodeArgs &a, cudaStream_t stream, bool programmatic);
+
+// Rotary positions at the append: the table of a rotary embedding, and the rotation of q and k
+// fused with the rotate + quantize + scatter of k and v.
+struct RopeTableArgs {
+    float *table;                // fp32 [num_positions][rotary_dim]: cosines, then sines
+    int64_t first_position, num_positions;
+    int32_t rotary_dim;
+    double turns[128];           // turns per position of each pair
+    double amplitude;
+};
+cudaError_t launch_rope_table(const RopeTableArgs &a, cudaStream_t stream);
+
+struct RopeAppendArgs {
+    RotateQuantizeArgs kv;       // k, v, slots and the cache (strides 0: contiguous)
+    const void *q;               // bf16 [T][Hq][D], tokens q_stride apart (0: contiguous)
+    void *q_out;                 // bf16 [T][Hq][D]
+    int64_t q_stride;
+    int32_t num_q_heads;
+    const int64_t *positions;    // [T]
+    const float *table;          // fp32 [num_positions][rotary_dim]
+    int64_t num_positions;
+    int32_t rotary_dim;
+    bool interleaved;
+    float *mass;                 // nullable: fp32 [num_pages][Hkv][16], zeroed at the new slots
+};
+cudaError_t launch_rope_append(const RopeAppendArgs &a, cudaStream_t stream);
+
+// Decode with accumulated attention weights (bf16 output, DecodeArgs::out_bf16).
+size_t decode_mass_workspace_bytes(int32_t num_kv_heads, int32_t num_q_heads, int32_t num_seqs,
+                                   int32_t max_blocks, int32_t head_dim);
+cudaError_t launch_paged_decode_mass(const DecodeArgs &a, float *mass, cudaStream_t stream,
+                                     bool programmatic);
+
+// Decode of a batch that shares a prefix (bf16 output): seq_lens and block_table are each
+// sequence's own tokens after it.
+size_t decode_prefix_workspace_bytes(int32_t num_kv_heads, int32_t num_q_heads, int32_t num_seqs,
+                                     int32_t prefix_len, int32_t head_dim);
+cudaError_t launch_paged_decode_prefix(const DecodeArgs &a, const int32_t *prefix_table,
+                                       int32_t prefix_len, cudaStream_t stream);
+
+struct EvictArgs {
+    uint8_t *kv_pages;
+    void *scales;
+    float *mass;                 // fp32 [num_pages][Hkv][16]
+    int32_t num_kv_heads, head_dim;
+    int64_t num_pages;
+    const int32_t *block_table;  // [S][max_blocks]
+    int32_t max_blocks;
+    const int32_t *seq_lens;     // [S]
+    int32_t num_seqs;
+    const int32_t *new_table;    // [S][new_blocks]
+    int32_t new_blocks;
+    int32_t *new_lens;           // [S]
+    int32_t *kept;               // [S][Hkv][keep]
+    int32_t keep, sink, recent;
+    uint32_t *status;
+};
+cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream);
 
 }  // namespace saw

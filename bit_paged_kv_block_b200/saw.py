@@ -31,6 +31,9 @@ SAW_DEV_BAD_PAGE = 0x2
 SAW_DEV_BAD_SEQ_LEN = 0x4
 SAW_DEV_WAIT_TIMEOUT = 0x8
 SAW_DEV_RANGE = 0x10
+SAW_DEV_BAD_POSITION = 0x20
+
+ROPE_KINDS = {"none": 0, "linear": 1, "ntk": 2, "banded": 3, "yarn": 4}
 
 
 class SawError(RuntimeError):
@@ -48,6 +51,18 @@ class saw_window_cache(ctypes.Structure):
     _fields_ = [("sink", ctypes.c_int32), ("recent", ctypes.c_int32), ("kv", ctypes.c_void_p),
                 ("num_pages", ctypes.c_int64), ("table", ctypes.c_void_p),
                 ("blocks", ctypes.c_int32)]
+
+
+class saw_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_positions", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("fast", ctypes.c_double), ("slow", ctypes.c_double),
+                ("amplitude", ctypes.c_double)]
+
+
+class saw_rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("num_positions", ctypes.c_int64),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 def _open_library() -> ctypes.CDLL:
@@ -113,6 +128,31 @@ def _open_library() -> ctypes.CDLL:
     lib.saw_decode_step_window.argtypes = [D, Wc, i32, P, P, P, P, P, P, i32, P, i32, f32, P, P,
                                            sz, P, P]
     lib.saw_decode_step_window.restype = ctypes.c_int
+    Rp = ctypes.POINTER(saw_rope)
+    lib.saw_rope_table.argtypes = [P, i64, i64, i32, ctypes.POINTER(saw_rope_scaling), P]
+    lib.saw_rope_rotate_quantize_paged.argtypes = [D, Rp, i32, P, i64, P, i64, P, i64, P, P, i64, P,
+                                                   P, P, P, P, P]
+    lib.saw_rope_quantize_paged_plain.argtypes = lib.saw_rope_rotate_quantize_paged.argtypes
+    lib.saw_paged_decode_prefix_workspace_bytes.argtypes = [D, i32, i32, i32]
+    lib.saw_paged_decode_attn_prefix.argtypes = [D, i32, P, P, P, P, i32, P, i32, P, i32, f32, P, P,
+                                                 sz, P, P]
+    lib.saw_paged_decode_attn_prefix_plain.argtypes = lib.saw_paged_decode_attn_prefix.argtypes
+    lib.saw_paged_decode_mass_workspace_bytes.argtypes = [D, i32, i32, i32]
+    lib.saw_paged_decode_attn_mass.argtypes = [D, i32, P, P, P, P, P, i32, P, i32, f32, P, P, sz, P,
+                                               P]
+    lib.saw_paged_decode_attn_mass_plain.argtypes = lib.saw_paged_decode_attn_mass.argtypes
+    lib.saw_evict_paged.argtypes = [D, P, P, P, P, i32, P, i32, P, i32, P, P, i32, i32, i32, P, P]
+    lib.saw_decode_step_rope.argtypes = [D, Rp, i32, P, P, P, P, P, P, P, P, P, i32, P, i32, f32, P,
+                                         P, sz, P, P]
+    lib.saw_decode_step_rope_mass.argtypes = [D, Rp, i32, P, P, P, P, P, P, P, P, P, P, i32, P, i32,
+                                              f32, P, P, sz, P, P]
+    for name in ("saw_rope_table", "saw_rope_rotate_quantize_paged", "saw_rope_quantize_paged_plain",
+                 "saw_paged_decode_attn_prefix", "saw_paged_decode_attn_prefix_plain",
+                 "saw_paged_decode_attn_mass", "saw_paged_decode_attn_mass_plain",
+                 "saw_evict_paged", "saw_decode_step_rope", "saw_decode_step_rope_mass"):
+        getattr(lib, name).restype = ctypes.c_int
+    lib.saw_paged_decode_prefix_workspace_bytes.restype = sz
+    lib.saw_paged_decode_mass_workspace_bytes.restype = sz
     return lib
 
 
@@ -639,3 +679,250 @@ def saw_decode_step_window(q, k_new, v_new, win, kv_pages, scales, block_table, 
                                     float(sm_scale), _ptr(out), _ptr(workspace), workspace.numel(),
                                     _ptr(dev_status), _stream(stream))
     _check(rc, "saw_decode_step_window")
+
+
+# ---- rotary positions --------------------------------------------------------------------------
+
+def rope_scaling(kind: str = "none", base: float = 10000.0, factor: float = 1.0,
+                 original_positions: float = 8192, low: float = 1.0, high: float = 4.0,
+                 fast: float = 32.0, slow: float = 1.0, amplitude: float = 0.0) -> saw_rope_scaling:
+    """The frequencies of a rotary table: kind "none", "linear", "ntk", "banded" (low, high: turns
+    over the original context) or "yarn" (fast, slow: its two turn counts); amplitude 0 is the
+    kind's own."""
+    if kind not in ROPE_KINDS:
+        raise ValueError(f"kind must be one of {sorted(ROPE_KINDS)}, got {kind!r}")
+    return saw_rope_scaling(ROPE_KINDS[kind], float(base), float(factor), float(original_positions),
+                            float(low), float(high), float(fast), float(slow), float(amplitude))
+
+
+def saw_rope_table(table, scaling: saw_rope_scaling, first_position: int = 0, stream=None) -> None:
+    """Fill a rotary table (fp32 [num_positions][rotary_dim]: cosines, then sines), row r for
+    position first_position + r."""
+    _need(table, "table", torch.float32, 2)
+    rc = lib.saw_rope_table(_ptr(table), int(first_position), table.shape[0], table.shape[1],
+                            ctypes.byref(scaling), _stream(stream))
+    _check(rc, "saw_rope_table")
+
+
+def _rope_desc(rope) -> saw_rope:
+    table, interleaved = rope
+    _need(table, "the rotary table", torch.float32, 2)
+    return saw_rope(table.data_ptr(), table.shape[0], table.shape[1], 1 if interleaved else 0)
+
+
+def _token_rows(t, name: str, tokens: int, heads, d: int) -> int:
+    """Check a token-strided [T][heads][D] bf16 view (heads of a token contiguous); its token
+    stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bf16 tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [T][heads][{d}] matching the cache, got {tuple(t.shape)}")
+    row = t.shape[1] * d
+    if t.shape[0] == 0 or row == 0:
+        return 0
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must have contiguous heads within a token")
+    return t.stride(0) if t.shape[0] > 1 else row
+
+
+def _cache_checks(kv_pages, scales, dev_status, mass=None):
+    _need(kv_pages, "kv_pages", torch.uint8, 5)
+    _need(scales, "scales", torch.float16, 5)
+    desc = cache_desc(kv_pages)
+    if tuple(scales.shape) != (desc.num_pages, desc.num_kv_heads, 2, PAGE_SIZE, 2):
+        raise ValueError("scales must be [num_pages][Hkv][2][16][2]")
+    if mass is not None:
+        _need(mass, "mass", torch.float32, 3)
+        if tuple(mass.shape) != (desc.num_pages, desc.num_kv_heads, PAGE_SIZE):
+            raise ValueError("mass must be [num_pages][Hkv][16]")
+    if dev_status is not None:
+        _need(dev_status, "dev_status", torch.int32, 1)
+    return desc
+
+
+def _rope_checks(q, k, v, positions, slot_mapping, q_out, desc):
+    _need(positions, "positions", torch.int64, 1)
+    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    T = slot_mapping.shape[0]
+    if positions.shape[0] != T:
+        raise ValueError("positions and slot_mapping must have one entry per token")
+    ks = _token_rows(k, "k", T, desc.num_kv_heads, desc.head_dim)
+    vs = _token_rows(v, "v", T, desc.num_kv_heads, desc.head_dim)
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        return T, 0, 0, ks, vs
+    qs = _token_rows(q, "q", T, None, desc.head_dim)
+    _need(q_out, "q_out", torch.bfloat16, 3)
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must be shaped as q")
+    return T, q.shape[1], qs, ks, vs
+
+
+def allocate_mass(num_pages: int, num_kv_heads: int, device="cuda") -> torch.Tensor:
+    """Accumulated attention weights of a cache, all 0: fp32 [P][Hkv][16]."""
+    return torch.zeros((num_pages, num_kv_heads, PAGE_SIZE), dtype=torch.float32, device=device)
+
+
+def saw_rope_rotate_quantize_paged(q, k, v, positions, slot_mapping, rope, q_out, kv_pages, scales,
+                                   mass=None, dev_status=None, stream=None, rotate=True) -> None:
+    """Rotate q and k (bf16 [T][heads][D], token-strided views allowed) by positions (int64 [T])
+    with rope = (table, interleaved), write q to q_out, and rotate, quantize and scatter k and v
+    into the cache; mass, when given, is set to 0 at the new slots.  q = q_out = None appends keys
+    alone.  rotate=False writes a plain INT4 cache."""
+    desc = _cache_checks(kv_pages, scales, dev_status, mass)
+    rp = _rope_desc(rope)
+    T, hq, qs, ks, vs = _rope_checks(q, k, v, positions, slot_mapping, q_out, desc)
+    fn = lib.saw_rope_rotate_quantize_paged if rotate else lib.saw_rope_quantize_paged_plain
+    rc = fn(ctypes.byref(desc), ctypes.byref(rp), hq, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
+            _ptr(positions), _ptr(slot_mapping), T, _ptr(q_out), _ptr(kv_pages), _ptr(scales),
+            _ptr(mass), _ptr(dev_status), _stream(stream))
+    _check(rc, "saw_rope_rotate_quantize_paged" if rotate else "saw_rope_quantize_paged_plain")
+
+
+# ---- decode for a batch that shares a prefix ---------------------------------------------------
+
+def saw_paged_decode_prefix_workspace_bytes(num_kv_heads: int, num_q_heads: int, num_seqs: int,
+                                            prefix_len: int, head_dim: int = HEAD_DIM) -> int:
+    desc = saw_cache_desc(int(num_kv_heads), int(head_dim), PAGE_SIZE, 1)
+    return int(lib.saw_paged_decode_prefix_workspace_bytes(ctypes.byref(desc), int(num_q_heads),
+                                                           int(num_seqs), int(prefix_len)))
+
+
+def allocate_prefix_workspace(num_kv_heads: int, num_q_heads: int, num_seqs: int, prefix_len: int,
+                              device="cuda", head_dim: int = HEAD_DIM) -> torch.Tensor:
+    n = saw_paged_decode_prefix_workspace_bytes(num_kv_heads, num_q_heads, num_seqs, prefix_len,
+                                                head_dim=head_dim)
+    if n == 0:
+        raise SawError(SAW_ERR_CUDA, "saw_paged_decode_prefix_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _decode_bf16_out_checks(q, block_table, seq_lens, out, workspace, desc):
+    _need(q, "q", torch.bfloat16, 3)
+    _need(out, "out", torch.bfloat16, 3)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(workspace, "workspace", torch.uint8, 1)
+    S, hq, d = q.shape
+    if d != desc.head_dim or out.shape != q.shape:
+        raise ValueError(f"q and out must be [S][Hq][{desc.head_dim}] matching the cache")
+    if block_table.shape[0] != S or seq_lens.shape[0] != S:
+        raise ValueError("block_table and seq_lens need one row per sequence")
+    return S, hq
+
+
+def saw_paged_decode_attn_prefix(q, kv_pages, scales, prefix_table, prefix_len, block_table,
+                                 seq_lens, out, workspace, sm_scale=None, dev_status=None,
+                                 stream=None, rotate=True) -> None:
+    """Decode attention of q (bf16 [S][Hq][D]) over a prefix that all sequences share (prefix_len
+    tokens in the pages of prefix_table, int32) and then each sequence's own seq_lens tokens, one
+    softmax over both, into out (bf16 [S][Hq][D])."""
+    desc = _cache_checks(kv_pages, scales, dev_status)
+    S, hq = _decode_bf16_out_checks(q, block_table, seq_lens, out, workspace, desc)
+    prefix_len = int(prefix_len)
+    if prefix_table is not None:
+        _need(prefix_table, "prefix_table", torch.int32, 1)
+    if prefix_len > PAGE_SIZE * (0 if prefix_table is None else prefix_table.shape[0]):
+        raise ValueError("prefix_table must hold a page for every 16 prefix tokens")
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(desc.head_dim)
+    fn = lib.saw_paged_decode_attn_prefix if rotate else lib.saw_paged_decode_attn_prefix_plain
+    rc = fn(ctypes.byref(desc), hq, _ptr(q), _ptr(kv_pages), _ptr(scales), _ptr(prefix_table),
+            prefix_len, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), S, float(sm_scale),
+            _ptr(out), _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream))
+    _check(rc, "saw_paged_decode_attn_prefix" if rotate else "saw_paged_decode_attn_prefix_plain")
+
+
+# ---- accumulated attention weights and eviction -------------------------------------------------
+
+def saw_paged_decode_mass_workspace_bytes(num_kv_heads: int, num_q_heads: int, num_seqs: int,
+                                          max_blocks: int, head_dim: int = HEAD_DIM) -> int:
+    desc = saw_cache_desc(int(num_kv_heads), int(head_dim), PAGE_SIZE, 1)
+    return int(lib.saw_paged_decode_mass_workspace_bytes(ctypes.byref(desc), int(num_q_heads),
+                                                         int(num_seqs), int(max_blocks)))
+
+
+def allocate_mass_workspace(num_kv_heads: int, num_q_heads: int, num_seqs: int, max_blocks: int,
+                            device="cuda", head_dim: int = HEAD_DIM) -> torch.Tensor:
+    n = saw_paged_decode_mass_workspace_bytes(num_kv_heads, num_q_heads, num_seqs, max_blocks,
+                                              head_dim=head_dim)
+    if n == 0:
+        raise SawError(SAW_ERR_CUDA, "saw_paged_decode_mass_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def saw_paged_decode_attn_mass(q, kv_pages, scales, mass, block_table, seq_lens, out, workspace,
+                               sm_scale=None, dev_status=None, stream=None, rotate=True) -> None:
+    """Decode attention of q (bf16 [S][Hq][D]) into out (bf16 [S][Hq][D]) that also adds every
+    cached token's attention weight, summed over the query heads of its kv head, to mass (fp32
+    [num_pages][Hkv][16])."""
+    if mass is None:
+        raise TypeError("mass must be a torch.Tensor")
+    desc = _cache_checks(kv_pages, scales, dev_status, mass)
+    S, hq = _decode_bf16_out_checks(q, block_table, seq_lens, out, workspace, desc)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(desc.head_dim)
+    fn = lib.saw_paged_decode_attn_mass if rotate else lib.saw_paged_decode_attn_mass_plain
+    rc = fn(ctypes.byref(desc), hq, _ptr(q), _ptr(kv_pages), _ptr(scales), _ptr(mass),
+            _ptr(block_table), block_table.shape[1], _ptr(seq_lens), S, float(sm_scale), _ptr(out),
+            _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream))
+    _check(rc, "saw_paged_decode_attn_mass" if rotate else "saw_paged_decode_attn_mass_plain")
+
+
+def saw_evict_paged(kv_pages, scales, mass, block_table, seq_lens, new_table, new_lens, kept,
+                    sink=0, recent=0, dev_status=None, stream=None) -> None:
+    """Bring each sequence down to kept.shape[2] tokens per kv head: the first `sink`, the last
+    `recent` and the heaviest between them (mass) move, in order, into the pages of new_table
+    (int32 [S][blocks]); new_lens (int32 [S]) and kept (int32 [S][Hkv][keep], old indices, -1 past
+    new_lens) are written.  The old pages are only read."""
+    if mass is None:
+        raise TypeError("mass must be a torch.Tensor")
+    desc = _cache_checks(kv_pages, scales, dev_status, mass)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(new_table, "new_table", torch.int32, 2)
+    _need(new_lens, "new_lens", torch.int32, 1)
+    _need(kept, "kept", torch.int32, 3)
+    S = seq_lens.shape[0]
+    if block_table.shape[0] != S or new_table.shape[0] != S or new_lens.shape[0] != S:
+        raise ValueError("block_table, new_table and new_lens need one row per sequence")
+    if tuple(kept.shape[:2]) != (S, desc.num_kv_heads):
+        raise ValueError("kept must be [S][Hkv][keep]")
+    rc = lib.saw_evict_paged(ctypes.byref(desc), _ptr(kv_pages), _ptr(scales), _ptr(mass),
+                             _ptr(block_table), block_table.shape[1], _ptr(seq_lens), S,
+                             _ptr(new_table), new_table.shape[1], _ptr(new_lens), _ptr(kept),
+                             kept.shape[2], int(sink), int(recent), _ptr(dev_status),
+                             _stream(stream))
+    _check(rc, "saw_evict_paged")
+
+
+def saw_decode_step_rope(q, k_new, v_new, positions, slot_mapping, rope, q_rot, kv_pages, scales,
+                         block_table, seq_lens, out, workspace, mass=None, sm_scale=None,
+                         dev_status=None, stream=None) -> None:
+    """One serving step on un-rotated q, k_new, v_new (bf16 [S][heads][D], contiguous):
+    saw_rope_rotate_quantize_paged (q to q_rot), then the decode.  Without mass:
+    saw_paged_decode_attn (out fp32, its workspace); with mass: saw_paged_decode_attn_mass (out
+    bf16, its workspace)."""
+    desc = _cache_checks(kv_pages, scales, dev_status, mass)
+    rp = _rope_desc(rope)
+    for t, name in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
+        _need(t, name, torch.bfloat16, 3)
+    _rope_checks(q, k_new, v_new, positions, slot_mapping, q_rot, desc)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(desc.head_dim)
+    head = (ctypes.byref(desc), ctypes.byref(rp), q.shape[1], _ptr(q), _ptr(k_new), _ptr(v_new),
+            _ptr(positions), _ptr(slot_mapping), _ptr(q_rot), _ptr(kv_pages), _ptr(scales))
+    if mass is None:
+        S, _ = _decode_checks(q_rot, kv_pages, scales, block_table, seq_lens, out, workspace,
+                              dev_status)[1:]
+        fn, name = lib.saw_decode_step_rope, "saw_decode_step_rope"
+    else:
+        S, _ = _decode_bf16_out_checks(q_rot, block_table, seq_lens, out, workspace, desc)
+        head += (_ptr(mass),)
+        fn, name = lib.saw_decode_step_rope_mass, "saw_decode_step_rope_mass"
+    rc = fn(*head, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), S, float(sm_scale),
+            _ptr(out), _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream))
+    _check(rc, name)

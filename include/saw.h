@@ -12,6 +12,10 @@
  *   saw_paged_decode_attn      decode attention over the INT4 paged cache (split-K, GQA)
  *   saw_decode_step            one serving step: append one token per sequence, then decode
  *
+ * and, beside them: the append with rotary positions (saw_rope_rotate_quantize_paged), the decode of a
+ * batch that shares a prefix (saw_paged_decode_attn_prefix), and a cache bounded by eviction
+ * (saw_paged_decode_attn_mass, saw_evict_paged).
+ *
  * Fixed build parameters (the pages give no numbers; these are the library's definition):
  *   head_dim D = 64, 128 or 256; Hadamard block B = min(D, 128) (a D = 256 vector is rotated
  *   as two independent 128-element blocks and keeps one (scale, zero) pair over all 256
@@ -84,6 +88,7 @@ typedef enum saw_status {
 #define SAW_DEV_WAIT_TIMEOUT 0x8u /* a bounded wait on a page copy gave up */
 #define SAW_DEV_RANGE 0x10u       /* a scale or zero point beyond fp16's range (|x| >= 65520) was
                                      stored as +-inf: that vector cannot be read back */
+#define SAW_DEV_BAD_POSITION 0x20u /* positions[t] outside the rotary table: token skipped */
 
 typedef struct saw_cache_desc {
     int32_t num_kv_heads; /* Hkv >= 1 */
@@ -355,6 +360,182 @@ int saw_decode_step_window(const saw_cache_desc *cache, const saw_window_cache *
                            int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t num_seqs,
                            float sm_scale, float *out, void *workspace, size_t workspace_bytes,
                            uint32_t *dev_status, void *stream);
+
+/* ---- rotary positions ------------------------------------------------------------------------
+ *
+ * A rotary embedding turns the pairs (a, b) of the first rotary_dim elements of a head vector at
+ * position p by the angle p f_i:
+ *     a' = a cos(p f_i) - b sin(p f_i),   b' = b cos(p f_i) + a sin(p f_i),   i < rotary_dim / 2,
+ * with pair i = elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when interleaved; the elements
+ * from rotary_dim on pass through.  Every product and sum is one IEEE fp32 operation (no fused
+ * multiply-add), and the result is rounded to bf16.
+ *
+ * The cosines and sines come from a table that a program fills once: fp32 [num_positions]
+ * [rotary_dim], rotary_dim / 2 cosines and then rotary_dim / 2 sines, row r for position
+ * first_position + r.  f_i = base^(-2 i / rotary_dim), scaled for long contexts by `kind`:
+ *     PLAIN   f_i
+ *     LINEAR  f_i / factor
+ *     NTK     base replaced by base factor^(rotary_dim / (rotary_dim - 2))
+ *     BANDED  with r_i = original_positions f_i / 2 pi turns over the original context and
+ *             t_i = clamp((r_i - low) / (high - low), 0, 1):  f_i ((1 - t_i) / factor + t_i)
+ *     YARN    with d(b) = rotary_dim ln(original_positions / (2 pi b)) / (2 ln base),
+ *             lo = max(0, floor d(fast)), hi = min(rotary_dim - 1, ceil d(slow)) and
+ *             t_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1):  f_i (t_i / factor + 1 - t_i),
+ *             and cosines and sines times amplitude (0: 0.1 ln factor + 1)
+ * (amplitude of the other kinds: 1 for 0, else as given).  Frequencies and angles are formed in
+ * fp64; the table agrees with the fp64 values to a few 1e-7. */
+#define SAW_ROPE_PLAIN 0
+#define SAW_ROPE_LINEAR 1
+#define SAW_ROPE_NTK 2
+#define SAW_ROPE_BANDED 3
+#define SAW_ROPE_YARN 4
+typedef struct saw_rope_scaling {
+    int32_t kind;              /* SAW_ROPE_* */
+    double base;               /* > 1 */
+    double factor;             /* >= 1 (PLAIN: unused) */
+    double original_positions; /* BANDED, YARN: > 0 */
+    double low, high;          /* BANDED: low < high */
+    double fast, slow;         /* YARN: > 0 */
+    double amplitude;          /* >= 0; 0: the kind's own */
+} saw_rope_scaling;
+
+/* Fill `table` (device, 16-byte aligned).  rotary_dim: a multiple of 16 up to 256;
+ * 0 <= first_position, first_position + num_positions <= 2^31. */
+int saw_rope_table(float *table, int64_t first_position, int64_t num_positions, int32_t rotary_dim,
+                   const saw_rope_scaling *scaling, void *stream);
+
+/* The rotary embedding an append applies: a table of positions 0 .. num_positions - 1. */
+typedef struct saw_rope {
+    const float *table;    /* device, fp32 [num_positions][rotary_dim], 16-byte aligned */
+    int64_t num_positions;
+    int32_t rotary_dim;    /* a multiple of 16, at most head_dim */
+    int32_t interleaved;   /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2 i, 2 i + 1) */
+} saw_rope;
+
+/* saw_rotate_quantize_paged for keys that still need their positions: rotates q and k by
+ * positions[t], writes q to q_out, and Hadamard-rotates, quantizes and scatters k and v; one launch.
+ * The cache gets exactly the bits that rounding the rotated keys to bf16 and appending them with
+ * saw_rotate_quantize_paged would give it.
+ *     q: bf16 [T][num_q_heads][D]; k, v: bf16 [T][Hkv][D]; positions, slot_mapping: int64 [T];
+ *     q_out: bf16 [T][num_q_heads][D], contiguous; it may be q itself when q is contiguous.
+ *     q_stride, k_stride, v_stride: bf16 elements between tokens (0: contiguous), multiples of 8;
+ *     k and v that are not contiguous need Hkv as saw_rotate_quantize_paged_strided does.
+ * num_q_heads = 0 (q, q_out unused) rotates and appends keys alone.  mass (or NULL): the accumulated
+ * weights below, fp32 [num_pages][Hkv][16], set to 0 at the new slots.  A token with a negative slot,
+ * a slot out of range (SAW_DEV_BAD_SLOT) or a position outside the table (SAW_DEV_BAD_POSITION) is
+ * skipped as a whole: its q_out row, cache rows and masses keep what they held.
+ * The _plain variant is the append of a plain INT4 cache (no Hadamard rotation). */
+int saw_rope_rotate_quantize_paged(const saw_cache_desc *cache, const saw_rope *rope,
+                                   int32_t num_q_heads, const void *q, int64_t q_stride,
+                                   const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                   const int64_t *positions, const int64_t *slot_mapping,
+                                   int64_t num_tokens, void *q_out, uint8_t *kv_pages, void *scales,
+                                   float *mass, uint32_t *dev_status, void *stream);
+int saw_rope_quantize_paged_plain(const saw_cache_desc *cache, const saw_rope *rope,
+                                  int32_t num_q_heads, const void *q, int64_t q_stride,
+                                  const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                  const int64_t *positions, const int64_t *slot_mapping,
+                                  int64_t num_tokens, void *q_out, uint8_t *kv_pages, void *scales,
+                                  float *mass, uint32_t *dev_status, void *stream);
+
+/* ---- decode for a batch that shares a prefix ---------------------------------------------------
+ *
+ * Every sequence attends over the prefix's prefix_len tokens, held once in the pages prefix_table
+ * (int32, device, ceil(prefix_len / 16) entries), and then over its own seq_lens[s] tokens (its row of
+ * block_table, starting on a page of its own); one softmax over both.  The prefix's pages are read for
+ * the whole batch together instead of once per sequence.  seq_lens[s] = 0 attends over the prefix
+ * alone; with prefix_len = 0 (prefix_table may be NULL) the call is a plain decode; a row that attends
+ * over nothing is zero, and so are the rows of a sequence whose length is out of range
+ * (SAW_DEV_BAD_SEQ_LEN).
+ * out: bf16 [S][Hq][D], rounded once at the end.  Arithmetic as saw_paged_decode_attn.  workspace: at
+ * least saw_paged_decode_prefix_workspace_bytes() for these sizes (a larger num_seqs or prefix_len
+ * covers a smaller one at the same heads), 256-byte aligned, no initialisation needed. */
+size_t saw_paged_decode_prefix_workspace_bytes(const saw_cache_desc *cache, int32_t num_q_heads,
+                                               int32_t num_seqs, int32_t prefix_len);
+int saw_paged_decode_attn_prefix(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
+                                 const uint8_t *kv_pages, const void *scales,
+                                 const int32_t *prefix_table, int32_t prefix_len,
+                                 const int32_t *block_table, int32_t max_blocks_per_seq,
+                                 const int32_t *seq_lens, int32_t num_seqs, float sm_scale, void *out,
+                                 void *workspace, size_t workspace_bytes, uint32_t *dev_status,
+                                 void *stream);
+int saw_paged_decode_attn_prefix_plain(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
+                                       const uint8_t *kv_pages, const void *scales,
+                                       const int32_t *prefix_table, int32_t prefix_len,
+                                       const int32_t *block_table, int32_t max_blocks_per_seq,
+                                       const int32_t *seq_lens, int32_t num_seqs, float sm_scale,
+                                       void *out, void *workspace, size_t workspace_bytes,
+                                       uint32_t *dev_status, void *stream);
+
+/* ---- accumulated attention weights and eviction -------------------------------------------------
+ *
+ * mass: fp32 [num_pages][Hkv][16], device, 16-byte aligned: per cached token and kv head, the
+ * attention weight it has received so far.  An append that is given the masses sets them to 0 at its
+ * slots; the decode below adds to them; the eviction keeps the heaviest tokens.
+ *
+ * saw_paged_decode_attn_mass: saw_paged_decode_attn with a bf16 output ([S][Hq][D], rounded once)
+ * that also adds, for every token t < seq_lens[s] of every sequence and kv head h,
+ *     mass[page][h][t mod 16] += sum over the G query heads of h of softmax(logits)_t.
+ * The weights are accurate to fp32's precision.  Each mass gets one add per sequence of the call that
+ * holds its page, so results repeat bit for bit unless sequences share a page, whose adds then happen
+ * in either order.  Slots past a sequence's end are not touched.  workspace: at least
+ * saw_paged_decode_mass_workspace_bytes() (it holds the logits of every page that the block table can
+ * name), 256-byte aligned, no initialisation needed. */
+size_t saw_paged_decode_mass_workspace_bytes(const saw_cache_desc *cache, int32_t num_q_heads,
+                                             int32_t num_seqs, int32_t max_blocks_per_seq);
+int saw_paged_decode_attn_mass(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
+                               const uint8_t *kv_pages, const void *scales, float *mass,
+                               const int32_t *block_table, int32_t max_blocks_per_seq,
+                               const int32_t *seq_lens, int32_t num_seqs, float sm_scale, void *out,
+                               void *workspace, size_t workspace_bytes, uint32_t *dev_status,
+                               void *stream);
+int saw_paged_decode_attn_mass_plain(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
+                                     const uint8_t *kv_pages, const void *scales, float *mass,
+                                     const int32_t *block_table, int32_t max_blocks_per_seq,
+                                     const int32_t *seq_lens, int32_t num_seqs, float sm_scale,
+                                     void *out, void *workspace, size_t workspace_bytes,
+                                     uint32_t *dev_status, void *stream);
+
+/* Bring sequences down to `keep` tokens.  Of sequence s (L = seq_lens[s] tokens in the pages of its
+ * block_table row), n = min(L, keep) tokens stay, chosen per kv head: the first `sink`, the last
+ * `recent`, and of those between them the keep - sink - recent with the largest mass (equal masses:
+ * the earlier token; a NaN or negative mass counts as 0).  In their order they are copied, codes,
+ * scales and masses as they are, to tokens 0 .. n - 1 in the pages of row s of new_table (int32
+ * [S][new_blocks]), whose other slots keep what they held; new_lens[s] = n; kept[s][h] (int32
+ * [S][Hkv][keep]) lists their old indices, -1 past n.  A sequence of at most `keep` tokens is copied
+ * whole.  Keys keep the positions they were rotated by.
+ * The old pages are only read, so they may be shared between sequences; the new ones must not be
+ * among them, nor appear twice, and new_lens must not be seq_lens.  A length out of range, or
+ * n > 16 * new_blocks, leaves the sequence out (SAW_DEV_BAD_SEQ_LEN, new_lens[s] = 0); a page id
+ * out of range skips its tokens (SAW_DEV_BAD_PAGE).  0 <= sink, 0 <= recent, 1 <= keep,
+ * sink + recent <= keep.  The cache may be a rotated or a plain INT4 one. */
+int saw_evict_paged(const saw_cache_desc *cache, uint8_t *kv_pages, void *scales, float *mass,
+                    const int32_t *block_table, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                    int32_t num_seqs, const int32_t *new_table, int32_t new_blocks,
+                    int32_t *new_lens, int32_t *kept, int32_t keep, int32_t sink, int32_t recent,
+                    uint32_t *dev_status, void *stream);
+
+/* Serving steps on an un-rotated q, k, v: saw_rope_rotate_quantize_paged on num_seqs tokens (one per
+ * sequence, contiguous rows; a skipped token's sequence still decodes, on what its q_rot row and
+ * cache hold), then the decode of q_rot (bf16 [S][Hq][D], written by the append), launched as a
+ * programmatic dependent.  saw_decode_step_rope decodes with saw_paged_decode_attn (fp32 out, its
+ * workspace); saw_decode_step_rope_mass with saw_paged_decode_attn_mass (bf16 out, its workspace),
+ * the append clearing the new slots' masses. */
+int saw_decode_step_rope(const saw_cache_desc *cache, const saw_rope *rope, int32_t num_q_heads,
+                         const void *q, const void *k_new, const void *v_new,
+                         const int64_t *positions, const int64_t *slot_mapping, void *q_rot,
+                         uint8_t *kv_pages, void *scales, const int32_t *block_table,
+                         int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t num_seqs,
+                         float sm_scale, float *out, void *workspace, size_t workspace_bytes,
+                         uint32_t *dev_status, void *stream);
+int saw_decode_step_rope_mass(const saw_cache_desc *cache, const saw_rope *rope, int32_t num_q_heads,
+                              const void *q, const void *k_new, const void *v_new,
+                              const int64_t *positions, const int64_t *slot_mapping, void *q_rot,
+                              uint8_t *kv_pages, void *scales, float *mass,
+                              const int32_t *block_table, int32_t max_blocks_per_seq,
+                              const int32_t *seq_lens, int32_t num_seqs, float sm_scale, void *out,
+                              void *workspace, size_t workspace_bytes, uint32_t *dev_status,
+                              void *stream);
 
 #ifdef __cplusplus
 } /* extern "C" */
