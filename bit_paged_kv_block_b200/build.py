@@ -22,10 +22,10 @@ COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE
 # per-file extra flags: the quantizer must not contract its IEEE operations into FMAs
 EXTRA = {"rotate_quantize.cu": ["-fmad=false"], "rope_append.cu": ["-fmad=false"]}
 SOURCES = ["rotate_quantize.cu", "paged_decode.cu", "paged_decode_bf16.cu", "prefill_tc.cu",
-           "rope_append.cu", "paged_decode_prefix.cu", "paged_decode_mass.cu", "evict.cu",
+           "rope_append.cu", "paged_decode_prefix.cu", "prefix_tc.cu", "paged_decode_mass.cu", "evict.cu",
            "saw_api.cu", "decode_static.cu"]
 HEADERS = ["saw_device.cuh", "saw_internal.h", "decode_common.cuh", "int4_format.cuh",
-           "quantize_device.cuh"]
+           "quantize_device.cuh", "tc_device.cuh", "prefix_tc.h"]
 
 
 def _nvcc() -> str:

@@ -12,9 +12,14 @@
 // one plan: kv head h of the prefix has S G query rows in blocks of 8, each block a segment over the
 // prefix's pages.  All pieces go to workspace slots; the prefix's are stored as rows, since the rows
 // of an output segment (sequence, kv head, up to 8 heads) may lie in two of its blocks.
+//
+// At D = 128 and from kTensorRows query rows per kv head on, the prefix is instead a kernel of its own on
+// the 5th-generation tensor cores (prefix_tc.cu), which the decode kernel over the own tokens runs
+// beside as its programmatic dependent, and the merge joins both kernels' pieces.
 #include <algorithm>
 
 #include "int4_format.cuh"
+#include "prefix_tc.h"
 
 namespace saw {
 namespace {
@@ -28,12 +33,19 @@ inline int64_t prefix_blocks(int32_t num_q_heads, int32_t num_kv_heads, int32_t 
     return (static_cast<int64_t>(num_seqs) * (num_q_heads / num_kv_heads) + kRowsPerBlock - 1) / kRowsPerBlock;
 }
 
+// The prefix's pieces where a kernel of its own wrote them: [Hkv][row_blocks][splits] (splits = 0: the
+// prefix is in the decode kernel's plan).
+struct PrefixPieces {
+    const float *slots;
+    int32_t row_blocks, splits;
+};
+
 // One CTA per output segment (sequence s, kv head h, block of up to 8 of its heads): fold the pieces
 // of the sequence's own tokens, then those of the prefix for the same query rows, and write the rows.
 // The warps take pieces in turn and warp 0 folds the warps' results in order, so the result does not
 // depend on timing.
 template <bool kRotate, int kD>
-__global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const DecodeParams p)
+__global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const DecodeParams p, const PrefixPieces pre)
 {
     using Fmt = PrefixFormat<kRotate, kD>;
     extern __shared__ uint8_t smem_raw[];
@@ -76,18 +88,27 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Decod
         sg.row0 = kRowsPerBlock * sg.b;
         sg.nrows = min(kRowsPerBlock, p.group - sg.row0);
         sg.qrow0 = s;
-        if (valid && p.prefix_seq >= 0) {
+        if (valid && (p.prefix_seq >= 0 || pre.splits > 0)) {
             const int ps = p.prefix_seq;
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 if (2 * t + e >= sg.nrows)
                     continue;
                 const int row = s * p.group + sg.row0 + 2 * t + e;
-                const int pj = sg.h * tb.nbk[ps] + row / kRowsPerBlock, pr = row % kRowsPerBlock;
-                const int64_t gseg = tb.spre[ps] + pj;
-                const int64_t u_hi = plan.warp_of_cost(plan.page_cost(ps, pj, tb.npg[ps] - 1));
-                for (int64_t u = plan.warp_of_cost(plan.page_cost(ps, pj, 0)) + warp; u <= u_hi; u += kMergeWarps) {
-                    const float *slot = p.partials + (gseg + u) * kSlot;
+                const int pr = row % kRowsPerBlock;
+                const float *slot0;
+                int pieces;
+                if (pre.splits > 0) {
+                    slot0 = pre.slots + (static_cast<int64_t>(sg.h) * pre.row_blocks + row / kRowsPerBlock) * pre.splits * kSlot;
+                    pieces = pre.splits;
+                } else {
+                    const int pj = sg.h * tb.nbk[ps] + row / kRowsPerBlock;
+                    const int64_t u_lo = plan.warp_of_cost(plan.page_cost(ps, pj, 0));
+                    slot0 = p.partials + (tb.spre[ps] + pj + u_lo) * kSlot;
+                    pieces = static_cast<int>(plan.warp_of_cost(plan.page_cost(ps, pj, tb.npg[ps] - 1)) - u_lo) + 1;
+                }
+                for (int k = warp; k < pieces; k += kMergeWarps) {
+                    const float *slot = slot0 + static_cast<int64_t>(k) * kSlot;
                     const float bm = slot[8 * kD + pr], bl = slot[8 * kD + 8 + pr];
                     const float4 *o4 = reinterpret_cast<const float4 *>(slot + pr * kD) + g;
                     const float mn = fmaxf(st.m[e], bm);
@@ -140,28 +161,42 @@ cudaError_t prefix_shape(size_t smem, size_t merge_smem, LaunchShape &out)
                                 smem, merge_smem, out);
 }
 
+// The fewest query rows per kv head (S G) that take the prefix to the tensor cores.
+constexpr int64_t kTensorRows = 24;
+
 // What a call launches, from its sizes alone (the workspace is sized by the same function).
 struct PrefixPlan {
     LaunchShape ls;
-    size_t smem, merge_smem, workspace;
+    size_t smem, merge_smem;
+    size_t tc_slots;         // byte offset of the tensor-core kernel's pieces in the workspace
+    size_t workspace;
     int64_t segments;
     int32_t plan_seqs;       // sequences of the decode kernel's plan
+    bool tensor;             // the prefix on the tensor cores (else in the plan)
+    PrefixTcShape tc;
 };
 
 template <int kD>
 cudaError_t prefix_plan(int32_t hkv, int32_t hq, int32_t num_seqs, int32_t prefix_len, PrefixPlan &pl)
 {
     using Fmt = PrefixFormat<true, kD>;
-    pl.plan_seqs = num_seqs + (prefix_len > 0 ? 1 : 0);
+    const int64_t rows = static_cast<int64_t>(num_seqs) * (hq / hkv);
+    pl.tensor = kD == 128 && prefix_len > 0 && rows >= kTensorRows;
+    pl.plan_seqs = num_seqs + (prefix_len > 0 && !pl.tensor ? 1 : 0);
     pl.smem = decode_smem_bytes<Fmt>(pl.plan_seqs, kRowsPerBlock);
     pl.merge_smem = merge_smem_bytes<Fmt::kTiles>(pl.plan_seqs);
     const cudaError_t e = prefix_shape<kD>(pl.smem, pl.merge_smem, pl.ls);
     if (e != cudaSuccess)
         return e;
-    pl.segments = max_segments(hkv, hq, num_seqs, 0, false) +
-                  (prefix_len > 0 ? hkv * prefix_blocks(hq, hkv, num_seqs) : 0);
-    pl.workspace = workspace_bytes_for<Fmt::kTiles>(
-        static_cast<size_t>(pl.ls.sms) * pl.ls.occ * Fmt::kWarps, pl.segments);
+    const int64_t own = max_segments(hkv, hq, num_seqs, 0, false), blocks = hkv * prefix_blocks(hq, hkv, num_seqs);
+    pl.segments = own + (pl.plan_seqs > num_seqs ? blocks : 0);
+    // slots of the plan's pieces (either with or without the prefix), then those of the tensor-core
+    // kernel: splits > 1 only while splits * hkv * row_pairs <= SMs, and a pair holds 32 row blocks
+    pl.tc_slots = workspace_bytes_for<Fmt::kTiles>(static_cast<size_t>(pl.ls.sms) * pl.ls.occ * Fmt::kWarps, own);
+    pl.workspace = pl.tc_slots + (blocks + (kD == 128 ? 32 * static_cast<int64_t>(pl.ls.sms) : 0)) *
+                                     slot_floats<Fmt::kTiles>() * sizeof(float);
+    if (pl.tensor)
+        pl.tc = prefix_tc_shape(hkv, rows, prefix_len, pl.ls.sms);
     return cudaSuccess;
 }
 
@@ -182,7 +217,7 @@ cudaError_t launch(const DecodeArgs &a, const int32_t *prefix_table, int32_t pre
     p.qrows = kRowsPerBlock;
     p.max_segments = pl.segments;
     p.total_warps = pl.ls.sms * pl.ls.occ * Fmt::kWarps;
-    p.prefix_seq = prefix_len > 0 ? a.num_seqs : -1;
+    p.prefix_seq = pl.plan_seqs > a.num_seqs ? a.num_seqs : -1;
     p.prefix_len = prefix_len;
     p.prefix_table = prefix_table;
 
@@ -195,7 +230,15 @@ cudaError_t launch(const DecodeArgs &a, const int32_t *prefix_table, int32_t pre
     cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 0;
+    PrefixPieces pre = {nullptr, 0, 0};
+    if (pl.tensor) {
+        float *slots = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + pl.tc_slots);
+        e = launch_prefix_tc(a, prefix_table, prefix_len, pl.tc, slots, stream);
+        if (e != cudaSuccess)
+            return e;
+        pre = {slots, pl.tc.row_blocks, pl.tc.splits};
+    }
+    cfg.numAttrs = pl.tensor ? 1 : 0;   // the own tokens run beside the prefix
     e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<Fmt, kModePrefix>, *map, p);
     if (e != cudaSuccess)
         return e;
@@ -204,7 +247,7 @@ cudaError_t launch(const DecodeArgs &a, const int32_t *prefix_table, int32_t pre
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = pl.merge_smem;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, prefix_merge_kernel<kRotate, kD>, p);
+    e = cudaLaunchKernelEx(&cfg, prefix_merge_kernel<kRotate, kD>, p, pre);
     if (e != cudaSuccess)
         return e;
     return cudaGetLastError();

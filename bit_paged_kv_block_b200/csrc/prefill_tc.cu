@@ -50,6 +50,7 @@
 
 #include "saw_device.cuh"
 #include "saw_internal.h"
+#include "tc_device.cuh"
 
 namespace saw {
 namespace {
@@ -62,7 +63,6 @@ constexpr float kTcHadamardC = 0.0883883461356163f;
 constexpr float kTcRescale = 0.0f;           // move the running max whenever a block exceeds it
 constexpr float kTcQScale = 256.0f;          // query entries enter the MMA scaled by 2^8
 constexpr float kTcPScale = 16.0f;           // weights enter the MMA scaled by 2^4
-constexpr uint64_t kTcWaitLimitNs = 1000000000ull;
 
 // shared memory (from a 1024-byte aligned base); 2 CTAs fit on an SM
 constexpr int kSmQ = 0;                                  // Q tile: 2 x [128 rows][128 B]
@@ -78,70 +78,6 @@ constexpr int kSmTile = kSmBars + 128;                   // tile descriptor
 constexpr int kSmBytes = kSmTile + 64;
 constexpr size_t kTcSmemBytes = 1024 + kSmBytes;
 constexpr uint32_t kTmemCols = 256;                      // O: columns 0..127, S: 128..255 (2 x 64)
-
-// byte offset of 16-bit element (row, k) in a tile of rows of 64 elements (128 B) per atom,
-// atom stride atom_bytes, 128-byte swizzle (16-byte chunk index XOR row mod 8)
-__device__ __forceinline__ uint32_t sw128_chunk(int row, int chunk16, uint32_t atom_bytes)
-{
-    return static_cast<uint32_t>((chunk16 >> 3) * atom_bytes + row * 128 + (((chunk16 & 7) ^ (row & 7)) << 4));
-}
-
-// tcgen05 shared-memory matrix descriptor: 128-byte swizzle, version 1 (sm_100), base offset 0
-__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lbo, uint32_t sbo)
-{
-    uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3FFF);
-    d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16;
-    d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFF) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
-}
-
-// instruction descriptor of kind::f16: fp16 A and B, fp32 accumulator, M x N, A / B K- or
-// MN-major
-__host__ __device__ constexpr uint32_t umma_idesc(int m, int n, int a_mn, int b_mn)
-{
-    return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
-           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
-}
-
-__device__ __forceinline__ void umma_f16(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(tmem_d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-                 : "memory");
-}
-
-__device__ __forceinline__ void umma_commit(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// 32 consecutive fp32 columns of this thread's tensor-memory lane
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float v[32])
-{
-    uint32_t r[32];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-                 "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-                   "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-                   "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-                   "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                 : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; i++)
-        v[i] = __uint_as_float(r[i]);
-}
-
 
 // tcgen05.ld.16x256b.x8 of one 16-lane half (32 columns per thread's pair of rows), waited for
 __device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t ta, float v[32])
@@ -179,9 +115,6 @@ __device__ __forceinline__ void stmatrix_x4(uint32_t addr, const uint32_t r[4])
                  "r"(r[2]), "r"(r[3])
                  : "memory");
 }
-
-// d order of the 8 entries of a 16-byte chunk: position j holds d = 8 a + kPerm[j]
-__host__ __device__ constexpr int chunk_d(int j) { return (j >> 1) + ((j & 1) << 2); }
 
 struct TcParams {
     const uint16_t *q;           // bf16 [total_q][Hq][128]
@@ -252,30 +185,6 @@ __device__ bool find_tile(const TcParams &p, int cta, int &s_out, int &h_out, in
     return true;
 }
 
-__device__ __forceinline__ void tc_arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// Bounded wait on phase `parity` of an mbarrier that also gives up once the other role has
-// (the shared abort flag); a timeout raises the flag.
-__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag)
-{
-    if (mbar_try_wait(bar, parity))
-        return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (true) {
-        if (mbar_try_wait(bar, parity))
-            return true;
-        if (*abort_flag != 0)
-            return false;
-        if (globaltimer_ns() - t0 > kTcWaitLimitNs) {
-            *abort_flag = 1;
-            return false;
-        }
-    }
-}
-
 // Named barrier of one role (128 threads: barrier 1 the producers, 2 the softmax warps) that
 // also ANDs a flag over them, so that the role leaves its loop as one.
 __device__ __forceinline__ bool role_bar_and(int id, bool v)
@@ -287,15 +196,6 @@ __device__ __forceinline__ bool role_bar_and(int id, bool v)
                  : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(kTcThreads / 2)
                  : "memory");
     return r != 0;
-}
-
-__device__ __forceinline__ uint4 ldg_nc16(const void *p)
-{
-    uint4 r;
-    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p));
-    return r;
 }
 
 // four fp16 pairs of the 8 codes of a 32-bit word as exact integers ((0x6400 | n) - 1024), stored

@@ -1,0 +1,554 @@
+// prefix_tc.cu -- the shared part of a shared-prefix decode (paged_decode_prefix.cu) on the
+// 5th-generation tensor cores: S G query rows of one kv head attend over the same prefix tokens, so
+// a tile of 128 rows is a dense M = 128 product with every block of the prefix.
+//
+// A CTA (one per SM) takes up to two tiles of 128 rows of one kv head and a run of 128-token blocks
+// (split-K over the prefix where there are fewer tiles than SMs), in four roles:
+//   - producers (warps 8-11) load the block's code words and (scale, zero) pairs into registers one
+//     block ahead and write dequantized fp16 tiles K^ = zero + code scale and V^ (128 tokens x 128 d,
+//     128-byte swizzle, two stages); both row tiles use them, so a page is unpacked once per 256 rows;
+//   - one thread of warp 12 issues S = Q K^T (M 128, N 128, K 128) and O += P V (the weights P from
+//     tensor memory, V^ the MN-major operand), for the two tiles in turn;
+//   - softmax warps (0-3: tile 0, 4-7: tile 1), one row per thread: the maximum of the row's 128
+//     logits, then 2^(s - m) as fp16 written over the logits in tensor memory.  While one tile's
+//     weights are formed, the other tile's products run.
+// Tensor memory (512 columns): O of the two tiles, then S / P of the two tiles.
+//
+// The running maximum moves only when a row exceeds it by kLag (log2 units): moving it rescales O in
+// tensor memory.  Weights enter as 2^(s - m + kLift) with kLag + kLift = 15, within fp16's range, and
+// flush to 0 only below 2^(-14 - kLift) of the reference (these tensor cores flush subnormals).  The
+// lift cancels: O and l carry it alike, and the piece's maximum is stored less it.
+// Dequantizing in the producers keeps every per-token factor out of the softmax (prefill_tc.cu applies
+// scales and zero points to the logits and weights instead: twice the instructions per element); the
+// price is one rounding of each cached value to fp16 (2^-11 relative at most, as for the query).
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "prefix_tc.h"
+#include "saw_device.cuh"
+#include "saw_internal.h"
+#include "tc_device.cuh"
+
+namespace saw {
+namespace {
+
+constexpr int kPtThreads = 13 * 32;
+constexpr int kPtProducers = 128;
+constexpr int kRows = 128;                   // M: rows of a tile
+constexpr int kTok = 128;                    // tokens of a block
+constexpr int kHalfTile = kTok * 128;        // bytes of one 64-wide half (128 B rows) of a tile
+constexpr float kHadC = 0.0883883461356163f;
+constexpr float kQLift = 16.0f;              // query entries enter scaled by 2^4, clear of subnormals
+constexpr float kLag = 4.0f;                 // log2: how far a row may exceed its reference maximum
+constexpr float kLift = 11.0f;
+
+// shared memory (from a 1024-byte aligned base)
+constexpr int kPtQ = 0;                               // 2 tiles x 2 halves x [128 rows][128 B]
+constexpr int kPtK = kPtQ + 2 * 2 * kHalfTile;        // 2 stages x 2 halves x [128 tokens][128 B]
+constexpr int kPtV = kPtK + 2 * 2 * kHalfTile;
+constexpr int kPtBars = kPtV + 2 * 2 * kHalfTile;     // 15 mbarriers, tensor-memory base, abort flag
+constexpr int kPtBytes = kPtBars + 256;
+constexpr size_t kPtSmem = 1024 + kPtBytes;
+
+// A from tensor memory: D[d] (+)= A[a] B[b]
+__device__ __forceinline__ void umma_f16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(tmem_d), "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// 32 columns of this thread's tensor-memory lane, queued; tmem_wait makes them readable
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t r[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+                 "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+                   "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+                   "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+                   "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+// wait for this thread's queued loads; the registers pass through so that no use moves above it
+__device__ __forceinline__ void tmem_wait(uint32_t r[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                   "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                   "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                   "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t r[32])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+                 "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                   "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+                   "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+                   "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+                   "r"(r[31])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t r[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+                 "%15,%16};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                   "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+                   "r"(r[15])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The 8 codes of a word as zero + code scale, in the pair order (d, d + 4), (d + 1, d + 5), ...: a
+// nibble ORed into the mantissa of 1024 (low nibble) or 64 (high nibble) is exact, and so is the
+// subtraction of the constant; the multiply-add rounds once.
+__device__ __forceinline__ void dequant_word_store(uint32_t dst, uint32_t w, __half2 scale, __half2 zero)
+{
+    const __half2 k1024 = u32_as_half2(0x64006400u), k64 = u32_as_half2(0x54005400u);
+    const uint32_t w8 = w >> 8;
+    const __half2 y0 = __hsub2(u32_as_half2((w & 0x000F000Fu) | 0x64006400u), k1024);
+    const __half2 y1 = __hsub2(u32_as_half2((w & 0x00F000F0u) | 0x54005400u), k64);
+    const __half2 y2 = __hsub2(u32_as_half2((w8 & 0x000F000Fu) | 0x64006400u), k1024);
+    const __half2 y3 = __hsub2(u32_as_half2((w8 & 0x00F000F0u) | 0x54005400u), k64);
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst),
+                 "r"(half2_as_u32(__hfma2(y0, scale, zero))), "r"(half2_as_u32(__hfma2(y1, scale, zero))),
+                 "r"(half2_as_u32(__hfma2(y2, scale, zero))), "r"(half2_as_u32(__hfma2(y3, scale, zero)))
+                 : "memory");
+}
+
+struct PrefixTcParams {
+    const uint16_t *q;           // bf16 [S][Hq][128]
+    const uint8_t *codes;
+    const uint8_t *scales;
+    const int32_t *table;        // prefix pages
+    float *slots;                // [Hkv][row_blocks][splits] pieces of 8 rows: O [8][128], m[8], l[8]
+    uint32_t *status;
+    int64_t num_pages;
+    int32_t len;                 // prefix tokens
+    int32_t hq, hkv, group, rows, row_blocks;
+    int32_t row_pairs;           // pairs of row tiles per kv head
+    int32_t splits, split_blocks;
+    float q_mult;
+};
+
+template <bool kRotate>
+__global__ void __launch_bounds__(kPtThreads, 1) prefix_tc_kernel(const PrefixTcParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bars = sbase + kPtBars;
+    // full / empty of the K and V stages, logits of a tile ready, weights of a tile ready, a tile's
+    // P V done, and the end of all products
+    auto k_full = [&](int s) { return bars + 8 * s; };
+    auto k_empty = [&](int s) { return bars + 16 + 8 * s; };
+    auto v_full = [&](int s) { return bars + 32 + 8 * s; };
+    auto v_empty = [&](int s) { return bars + 48 + 8 * s; };
+    auto s_full = [&](int t) { return bars + 64 + 8 * t; };
+    auto p_full = [&](int t) { return bars + 80 + 8 * t; };
+    auto o_done = [&](int t) { return bars + 96 + 8 * t; };
+    const uint32_t all_done = bars + 112;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kPtBars + 128);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kPtBars + 132);
+
+    pdl_launch_dependents();   // the batch's own tokens do not depend on this kernel
+    const int h = blockIdx.x % p.hkv, rest = blockIdx.x / p.hkv;
+    const int pair = rest % p.row_pairs, split = rest / p.row_pairs;
+    const int row0 = pair * 2 * kRows;
+    const int tiles = p.rows - row0 > kRows ? 2 : 1;
+    const int first = split * p.split_blocks * kTok;                       // first token
+    const int n_tok = min(p.len - first, p.split_blocks * kTok);           // >= 1
+    const int nb = (n_tok + kTok - 1) / kTok;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; i++) {
+            mbar_init(k_full(i), kPtProducers);
+            mbar_init(v_full(i), kPtProducers);
+            mbar_init(k_empty(i), 1);
+            mbar_init(v_empty(i), 1);
+            mbar_init(s_full(i), 1);
+            mbar_init(p_full(i), kRows);
+            mbar_init(o_done(i), 1);
+        }
+        mbar_init(all_done, 1);
+        *abort_flag = 0;
+    }
+    mbar_init_fence();
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(tmem_slot)), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+
+    // ---- the query tiles: rotate, scale, fp16, in the codes' d order (a thread per row) -----------
+    if (warp < 8) {
+        const int r = row0 + tid;
+        const bool live = r < p.rows;
+        const int seq = live ? r / p.group : 0, head = live ? r - seq * p.group : 0;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            p.q + (static_cast<int64_t>(seq) * p.hq + h * p.group + head) * 128);
+#pragma unroll 1
+        for (int hf = 0; hf < 2; hf++) {
+            float x[64];
+#pragma unroll
+            for (int c = 0; c < 8; c++) {
+                const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
+                const uint4 ua = live ? src[c] : zero4, ub = live ? src[8 + c] : zero4;
+                const uint32_t wa[4] = {ua.x, ua.y, ua.z, ua.w}, wb[4] = {ub.x, ub.y, ub.z, ub.w};
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const float a = __uint_as_float(e ? (wa[k] & 0xFFFF0000u) : (wa[k] << 16));
+                        const float b = __uint_as_float(e ? (wb[k] & 0xFFFF0000u) : (wb[k] << 16));
+                        x[8 * c + 2 * k + e] = !kRotate ? (hf ? b : a) : (hf ? a - b : a + b);
+                    }
+            }
+#pragma unroll
+            for (int hb = 1; kRotate && hb < 64; hb <<= 1)
+#pragma unroll
+                for (int i = 0; i < 64; i++)
+                    if ((i & hb) == 0) {
+                        const float a = x[i], b = x[i + hb];
+                        x[i] = a + b;
+                        x[i + hb] = a - b;
+                    }
+            const uint32_t tile = sbase + kPtQ + (tid >> 7) * 2 * kHalfTile;
+#pragma unroll
+            for (int c = 0; c < 8; c++) {
+                uint32_t wv[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    wv[k] = half2_as_u32(__floats2half2_rn(x[8 * c + chunk_d(2 * k)] * (p.q_mult * kQLift),
+                                                           x[8 * c + chunk_d(2 * k + 1)] * (p.q_mult * kQLift)));
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile + sw128_chunk(tid & 127, 8 * hf + c, kHalfTile)),
+                             "r"(wv[0]), "r"(wv[1]), "r"(wv[2]), "r"(wv[3]) : "memory");
+            }
+        }
+        async_proxy_fence();   // the tile is read by the tensor cores
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto o_col = [&](int t) { return tmem + 128u * t; };
+    auto s_col = [&](int t) { return tmem + 256u + 128u * t; };
+
+    if (warp >= 8 && warp < 12) {
+        // ======== producers ==========================================================================
+        // Lane -> (row of 8, 16-byte quarter of the 64-byte code row) such that the 8 lanes of a store
+        // phase (4 rows x 2 adjacent quarters) hit 8 different 16-byte columns of the swizzled tile.
+        const int pw = warp - 8;
+        const int q4 = (lane & 1) | (((lane >> 3) & 1) << 1);
+        const int r8 = ((lane >> 1) & 3) | ((lane >> 4) << 2);
+        const int rk = 8 * (pw & 1) + r8;          // token within its page
+        const int pg = pw >> 1;                    // pages pg + 2 i of a block
+        const int n_pages = (p.len + kPageSize - 1) / kPageSize, page0 = first / kPageSize;
+        struct Words {
+            uint4 k[4], v[4];
+            uint32_t sk[4], sv[4];
+        };
+        auto ids = [&](int b, int32_t id[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int j = page0 + 8 * b + pg + 2 * i;
+                id[i] = j < n_pages ? __ldg(p.table + j) : -1;
+                if (j < n_pages && (id[i] < 0 || id[i] >= p.num_pages)) {
+                    set_status(p.status, SAW_DEV_BAD_PAGE);
+                    id[i] = 0;
+                }
+            }
+        };
+        auto fetch = [&](int b, const int32_t id[4], Words &w) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int64_t at = static_cast<int64_t>(max(id[i], 0)) * p.hkv + h;
+                const uint8_t *c = p.codes + at * 2048 + rk * 64 + q4 * 16;
+                const uint8_t *s = p.scales + at * 128 + rk * 4;
+                w.k[i] = ldg_nc16(c);
+                w.v[i] = ldg_nc16(c + 1024);
+                // tokens past the prefix: scale and zero 0, so K^ and V^ are 0 whatever the rows hold
+                const bool in = first + kTok * b + kPageSize * (pg + 2 * i) + rk < p.len;
+                w.sk[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(s)) : 0u;
+                w.sv[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(s + 64)) : 0u;
+            }
+        };
+        auto unpack = [&](uint32_t tile, const uint4 w[4], const uint32_t sz[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int row = kPageSize * (pg + 2 * i) + rk;
+                const __half2 scale = u32_as_half2(__byte_perm(sz[i], 0, 0x1010));
+                const __half2 zero = u32_as_half2(__byte_perm(sz[i], 0, 0x3232));
+                dequant_word_store(tile + sw128_chunk(row, 4 * q4 + 0, kHalfTile), w[i].x, scale, zero);
+                dequant_word_store(tile + sw128_chunk(row, 4 * q4 + 1, kHalfTile), w[i].y, scale, zero);
+                dequant_word_store(tile + sw128_chunk(row, 4 * q4 + 2, kHalfTile), w[i].z, scale, zero);
+                dequant_word_store(tile + sw128_chunk(row, 4 * q4 + 3, kHalfTile), w[i].w, scale, zero);
+            }
+        };
+        int32_t id[4];
+        Words cur, nxt;
+        ids(0, id);
+        fetch(0, id, cur);
+        if (nb > 1)
+            ids(1, id);
+        for (int kb = 0; kb < nb; kb++) {
+            if (kb + 1 < nb)
+                fetch(kb + 1, id, nxt);
+            if (kb + 2 < nb)
+                ids(kb + 2, id);
+            const int st = kb & 1;
+            const uint32_t parity = static_cast<uint32_t>((kb - 2) >> 1) & 1u;
+            if (kb >= 2 && !tc_wait(k_empty(st), parity, abort_flag))
+                break;
+            unpack(sbase + kPtK + st * 2 * kHalfTile, cur.k, cur.sk);
+            async_proxy_fence();
+            tc_arrive(k_full(st));
+            if (kb >= 2 && !tc_wait(v_empty(st), parity, abort_flag))
+                break;
+            unpack(sbase + kPtV + st * 2 * kHalfTile, cur.v, cur.sv);
+            async_proxy_fence();
+            tc_arrive(v_full(st));
+            cur = nxt;
+        }
+    } else if (warp == 12) {
+        // ======== the products =========================================================================
+        if (lane == 0) {
+            constexpr uint32_t id_qk = umma_idesc(kRows, kTok, 0, 0);
+            constexpr uint32_t id_pv = umma_idesc(kRows, 128, 0, 1);
+            auto issue_qk = [&](int t, int kb) {
+                const uint32_t q = sbase + kPtQ + t * 2 * kHalfTile, k = sbase + kPtK + (kb & 1) * 2 * kHalfTile;
+#pragma unroll
+                for (int ks = 0; ks < 8; ks++) {
+                    const uint32_t off = (ks >> 2) * kHalfTile + (ks & 3) * 32;
+                    umma_f16(s_col(t), umma_desc(q + off, 16, 1024), umma_desc(k + off, 16, 1024), id_qk, ks > 0);
+                }
+                umma_commit(s_full(t));
+            };
+            auto issue_pv = [&](int t, int kb) {
+                const uint32_t v = sbase + kPtV + (kb & 1) * 2 * kHalfTile;
+#pragma unroll
+                for (int ks = 0; ks < 8; ks++)
+                    umma_f16_ta(o_col(t), s_col(t) + 8 * ks, umma_desc(v + ks * 2048, kHalfTile, 1024), id_pv,
+                                kb > 0 || ks > 0);
+                umma_commit(o_done(t));
+            };
+            bool ok = tc_wait(k_full(0), 0, abort_flag);
+            if (ok) {
+                tc_fence_after();
+                for (int t = 0; t < tiles; t++)
+                    issue_qk(t, 0);
+                umma_commit(k_empty(0));
+            }
+            for (int kb = 0; ok && kb < nb; kb++) {
+                const uint32_t par = static_cast<uint32_t>(kb) & 1u, par2 = static_cast<uint32_t>(kb >> 1) & 1u;
+                for (int t = 0; ok && t < tiles; t++) {
+                    ok = (t > 0 || tc_wait(v_full(kb & 1), par2, abort_flag)) && tc_wait(p_full(t), par, abort_flag);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    issue_pv(t, kb);
+                    if (t == tiles - 1)
+                        umma_commit(v_empty(kb & 1));
+                    if (kb + 1 < nb) {
+                        // the next logits overwrite this block's weights: once P V has read them
+                        ok = (t > 0 || tc_wait(k_full((kb + 1) & 1), static_cast<uint32_t>((kb + 1) >> 1) & 1u, abort_flag)) &&
+                             tc_wait(o_done(t), par, abort_flag);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        issue_qk(t, kb + 1);
+                        if (t == tiles - 1)
+                            umma_commit(k_empty((kb + 1) & 1));
+                    }
+                }
+            }
+            // every product and its arrivals are over before shared and tensor memory are released
+            umma_commit(all_done);
+            mbar_wait_bounded(all_done, 0, kTcWaitLimitNs / 10);
+        }
+    } else if (warp < 8 && (warp >> 2) < tiles) {
+        // ======== softmax: one row per thread ===========================================================
+        const int t = warp >> 2;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t so = s_col(t) + lanes, oo = o_col(t) + lanes;
+        const int r = row0 + tid;
+        float m_ref = -INFINITY;
+        uint64_t l2 = f2_pack(0.0f, 0.0f);
+        const uint64_t unlift = f2_pack(1.0f / kQLift, 1.0f / kQLift);
+        bool ok = true;
+        for (int kb = 0; kb < nb; kb++) {
+            ok = tc_wait(s_full(t), static_cast<uint32_t>(kb) & 1u, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok)
+                break;
+            tc_fence_after();
+            const int valid = n_tok - kTok * kb;   // tokens of the block that exist (more: all)
+            uint32_t a[32], b[32];
+            // the row's maximum
+            float mx = -INFINITY;
+            tmem_ld32_async(so, a);
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                uint32_t *x = (c & 1) ? b : a;
+                tmem_wait(x);
+                if (c < 3)
+                    tmem_ld32_async(so + 32 * (c + 1), (c & 1) ? a : b);
+                if (valid < 32 * (c + 1)) {
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        mx = 32 * c + i < valid ? fmaxf(mx, __uint_as_float(x[i])) : mx;
+                } else {
+                    float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        m4[(i >> 1) & 3] = fmax3(m4[(i >> 1) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                    mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+                }
+            }
+            mx *= 1.0f / kQLift;
+            const bool grow = mx > m_ref + kLag;
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+                const float alpha = grow ? ex2_approx(m_ref - mx) : 1.0f;   // 0 on the first block
+                if (grow)
+                    m_ref = mx;
+                l2 = f2_mul(l2, f2_pack(alpha, alpha));
+                if (kb > 0) {   // (O of the blocks before this one is complete: their P V precede these logits)
+                    const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+                    for (int c = 0; c < 4; c++) {
+                        tmem_ld32_async(oo + 32 * c, a);
+                        tmem_wait(a);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float x0, x1;
+                            f2_unpack(f2_mul(f2_pack(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), a2), x0, x1);
+                            a[i] = __float_as_uint(x0);
+                            a[i + 1] = __float_as_uint(x1);
+                        }
+                        tmem_st32(oo + 32 * c, a);
+                    }
+                    tmem_wait_st();
+                }
+            }
+            // the weights, over the logits' first 64 columns (chunk c's weights take columns
+            // 16 c .. 16 c + 15, whose logits have been read by then)
+            const float shift = kLift - m_ref;
+            const uint64_t sh2 = f2_pack(shift, shift);
+            tmem_ld32_async(so, a);
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                uint32_t *x = (c & 1) ? b : a;
+                tmem_wait(x);
+                if (c < 3)
+                    tmem_ld32_async(so + 32 * (c + 1), (c & 1) ? a : b);
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    float y0, y1;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), unlift, sh2), y0, y1);
+                    float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
+                    if (valid < 32 * (c + 1)) {
+                        e0 = 32 * c + i < valid ? e0 : 0.0f;
+                        e1 = 32 * c + i + 1 < valid ? e1 : 0.0f;
+                    }
+                    l2 = f2_add(l2, f2_pack(e0, e1));
+                    w[i >> 1] = half2_as_u32(__floats2half2_rn(e0, e1));
+                }
+                tmem_st16(so + 16 * c, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            tc_arrive(p_full(t));
+        }
+        // ---- the piece: O, m, l of this row ---------------------------------------------------------
+        ok = ok && tc_wait(o_done(t), static_cast<uint32_t>(nb - 1) & 1u, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (ok) {
+            tc_fence_after();
+            float *slot = p.slots + ((static_cast<int64_t>(h) * p.row_blocks + (r >> 3)) * p.splits + split) * (8 * 128 + 16);
+            float la, lb;
+            f2_unpack(l2, la, lb);
+            if (r < p.rows) {
+                slot[8 * 128 + (r & 7)] = m_ref - kLift;
+                slot[8 * 128 + 8 + (r & 7)] = la + lb;
+            }
+#pragma unroll 1
+            for (int c = 0; c < 4; c++) {
+                uint32_t o[32];
+                tmem_ld32_async(oo + 32 * c, o);
+                tmem_wait(o);
+                if (r < p.rows) {
+                    float4 *dst = reinterpret_cast<float4 *>(slot + (r & 7) * 128 + 32 * c);
+#pragma unroll
+                    for (int g = 0; g < 4; g++) {   // d = 8 g + (0 .. 7) sits in columns 0, 2, 4, 6, 1, 3, 5, 7
+                        dst[2 * g] = make_float4(__uint_as_float(o[8 * g]), __uint_as_float(o[8 * g + 2]),
+                                                 __uint_as_float(o[8 * g + 4]), __uint_as_float(o[8 * g + 6]));
+                        dst[2 * g + 1] = make_float4(__uint_as_float(o[8 * g + 1]), __uint_as_float(o[8 * g + 3]),
+                                                     __uint_as_float(o[8 * g + 5]), __uint_as_float(o[8 * g + 7]));
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (tid == 0 && *abort_flag != 0)
+        set_status(p.status, SAW_DEV_WAIT_TIMEOUT);
+    if (warp == 12)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+}  // namespace
+
+PrefixTcShape prefix_tc_shape(int32_t num_kv_heads, int64_t rows, int32_t prefix_len, int32_t sms)
+{
+    PrefixTcShape s;
+    s.row_blocks = static_cast<int32_t>((rows + 7) / 8);
+    s.row_pairs = static_cast<int32_t>((rows + 2 * kRows - 1) / (2 * kRows));
+    const int64_t blocks = (static_cast<int64_t>(prefix_len) + kTok - 1) / kTok;
+    const int64_t room = std::max<int64_t>(1, sms / (static_cast<int64_t>(num_kv_heads) * s.row_pairs));
+    s.split_blocks = static_cast<int32_t>((blocks + room - 1) / room);
+    s.splits = static_cast<int32_t>((blocks + s.split_blocks - 1) / s.split_blocks);
+    return s;
+}
+
+cudaError_t launch_prefix_tc(const DecodeArgs &a, const int32_t *prefix_table, int32_t prefix_len,
+                             const PrefixTcShape &s, float *slots, cudaStream_t stream)
+{
+    PrefixTcParams p;
+    p.q = static_cast<const uint16_t *>(a.q);
+    p.codes = a.kv_pages;
+    p.scales = static_cast<const uint8_t *>(a.scales);
+    p.table = prefix_table;
+    p.slots = slots;
+    p.status = a.status;
+    p.num_pages = a.num_pages;
+    p.len = prefix_len;
+    p.hq = a.num_q_heads;
+    p.hkv = a.num_kv_heads;
+    p.group = a.num_q_heads / a.num_kv_heads;
+    p.rows = a.num_seqs * p.group;
+    p.row_blocks = s.row_blocks;
+    p.row_pairs = s.row_pairs;
+    p.splits = s.splits;
+    p.split_blocks = s.split_blocks;
+    // q carries sm_scale * log2(e) and 1/sqrt(128) of the unnormalised butterfly
+    p.q_mult = static_cast<float>((a.rotate ? static_cast<double>(kHadC) : 1.0) * a.sm_scale * 1.4426950408889634);
+    auto *kernel = a.rotate ? prefix_tc_kernel<true> : prefix_tc_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPtSmem));
+    if (e != cudaSuccess)
+        return e;
+    kernel<<<static_cast<unsigned>(s.splits * s.row_pairs * p.hkv), kPtThreads, kPtSmem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace saw

@@ -9,6 +9,7 @@ if that fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -177,14 +178,20 @@ def _check(rc: int, where: str) -> None:
         raise SawError(rc, where)
 
 
-def _ptr(t) -> ctypes.c_void_p:
-    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+# the current stream's handle without building a Stream object (3 us a call), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _need(t: torch.Tensor, name: str, dtype, ndim=None, cuda=True) -> None:
@@ -192,7 +199,7 @@ def _need(t: torch.Tensor, name: str, dtype, ndim=None, cuda=True) -> None:
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if cuda and t.device.type != "cuda":
+    if cuda and not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions, got {tuple(t.shape)}")
@@ -698,7 +705,9 @@ def rope_scaling(kind: str = "none", base: float = 10000.0, factor: float = 1.0,
 def saw_rope_table(table, scaling: saw_rope_scaling, first_position: int = 0, stream=None) -> None:
     """Fill a rotary table (fp32 [num_positions][rotary_dim]: cosines, then sines), row r for
     position first_position + r."""
-    _need(table, "table", torch.float32, 2)
+    if table is None:
+        raise TypeError("table must be a torch.Tensor")
+    _need_here((table, "table", torch.float32, 2))
     rc = lib.saw_rope_table(_ptr(table), int(first_position), table.shape[0], table.shape[1],
                             ctypes.byref(scaling), _stream(stream))
     _check(rc, "saw_rope_table")
@@ -706,56 +715,84 @@ def saw_rope_table(table, scaling: saw_rope_scaling, first_position: int = 0, st
 
 def _rope_desc(rope) -> saw_rope:
     table, interleaved = rope
-    _need(table, "the rotary table", torch.float32, 2)
-    return saw_rope(table.data_ptr(), table.shape[0], table.shape[1], 1 if interleaved else 0)
+    if table is None:
+        raise TypeError("the rotary table must be a torch.Tensor")
+    _need_here((table, "the rotary table", torch.float32, 2))
+    positions, rotary = table.shape
+    return saw_rope(table.data_ptr(), positions, rotary, 1 if interleaved else 0)
+
+
+def _need_here(*specs) -> None:
+    """_need for (tensor, name, dtype, dimensions) of one call, whose tensors must all be on the
+    current CUDA device: the library launches there."""
+    device = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    for t, name, dtype, ndim in specs:
+        if t is None:
+            continue
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.dim() == ndim
+                and t.is_contiguous()):
+            _need(t, name, dtype, ndim)
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on the current device (cuda:{device}), got {t.device}")
 
 
 def _token_rows(t, name: str, tokens: int, heads, d: int) -> int:
-    """Check a token-strided [T][heads][D] bf16 view (heads of a token contiguous); its token
-    stride."""
+    """Check a token-strided [T][heads][D] bf16 view on the current device (heads of a token
+    contiguous); its token stride."""
     if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be a bf16 tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [T][heads][{d}] matching the cache, got {tuple(t.shape)}")
-    row = t.shape[1] * d
-    if t.shape[0] == 0 or row == 0:
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != d or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [T][heads][{d}] matching the cache, got {tuple(shape)}")
+    if t.is_contiguous():
         return 0
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+    st, sh, se = t.stride()
+    if se != 1 or (shape[1] > 1 and sh != d):
         raise ValueError(f"{name} must have contiguous heads within a token")
-    return t.stride(0) if t.shape[0] > 1 else row
+    return st if tokens > 1 else 0
+
+
+@functools.lru_cache(maxsize=256)
+def _cache_desc_of(num_pages: int, hkv: int, two: int, page: int, half: int) -> saw_cache_desc:
+    if two != 2 or half * 2 not in (64, 128, 256):
+        raise ValueError(f"kv_pages must be [num_pages][Hkv][2][16][D / 2], got "
+                         f"{(num_pages, hkv, two, page, half)}")
+    return saw_cache_desc(hkv, half * 2, page, num_pages)
 
 
 def _cache_checks(kv_pages, scales, dev_status, mass=None):
-    _need(kv_pages, "kv_pages", torch.uint8, 5)
-    _need(scales, "scales", torch.float16, 5)
-    desc = cache_desc(kv_pages)
-    if tuple(scales.shape) != (desc.num_pages, desc.num_kv_heads, 2, PAGE_SIZE, 2):
+    """Check a cache's tensors; its descriptor (shared between calls: not to be changed)."""
+    _need_here((kv_pages, "kv_pages", torch.uint8, 5), (scales, "scales", torch.float16, 5),
+               (mass, "mass", torch.float32, 3), (dev_status, "dev_status", torch.int32, 1))
+    if kv_pages is None or scales is None:
+        raise TypeError("kv_pages and scales must be torch.Tensors")
+    pages, hkv, two, page, half = kv_pages.shape
+    desc = _cache_desc_of(pages, hkv, two, page, half)
+    if scales.shape != (pages, hkv, 2, PAGE_SIZE, 2):
         raise ValueError("scales must be [num_pages][Hkv][2][16][2]")
-    if mass is not None:
-        _need(mass, "mass", torch.float32, 3)
-        if tuple(mass.shape) != (desc.num_pages, desc.num_kv_heads, PAGE_SIZE):
-            raise ValueError("mass must be [num_pages][Hkv][16]")
-    if dev_status is not None:
-        _need(dev_status, "dev_status", torch.int32, 1)
+    if mass is not None and mass.shape != (pages, hkv, PAGE_SIZE):
+        raise ValueError("mass must be [num_pages][Hkv][16]")
     return desc
 
 
 def _rope_checks(q, k, v, positions, slot_mapping, q_out, desc):
-    _need(positions, "positions", torch.int64, 1)
-    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    if positions is None or slot_mapping is None:
+        raise TypeError("positions and slot_mapping must be torch.Tensors")
+    _need_here((positions, "positions", torch.int64, 1), (slot_mapping, "slot_mapping", torch.int64, 1),
+               (q_out, "q_out", torch.bfloat16, 3))
     T = slot_mapping.shape[0]
     if positions.shape[0] != T:
         raise ValueError("positions and slot_mapping must have one entry per token")
-    ks = _token_rows(k, "k", T, desc.num_kv_heads, desc.head_dim)
-    vs = _token_rows(v, "v", T, desc.num_kv_heads, desc.head_dim)
-    if q is None:
-        if q_out is not None:
-            raise ValueError("q_out without q")
+    hkv, d = desc.num_kv_heads, desc.head_dim
+    ks = _token_rows(k, "k", T, hkv, d)
+    vs = _token_rows(v, "v", T, hkv, d)
+    if q is None or q_out is None:
+        if q is not q_out:
+            raise ValueError("q and q_out go together")
         return T, 0, 0, ks, vs
-    qs = _token_rows(q, "q", T, None, desc.head_dim)
-    _need(q_out, "q_out", torch.bfloat16, 3)
+    qs = _token_rows(q, "q", T, None, d)
     if q_out.shape != q.shape:
         raise ValueError("q_out must be shaped as q")
     return T, q.shape[1], qs, ks, vs
@@ -801,13 +838,14 @@ def allocate_prefix_workspace(num_kv_heads: int, num_q_heads: int, num_seqs: int
 
 
 def _decode_bf16_out_checks(q, block_table, seq_lens, out, workspace, desc):
-    _need(q, "q", torch.bfloat16, 3)
-    _need(out, "out", torch.bfloat16, 3)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    _need(workspace, "workspace", torch.uint8, 1)
-    S, hq, d = q.shape
-    if d != desc.head_dim or out.shape != q.shape:
+    if q is None or out is None or block_table is None or seq_lens is None or workspace is None:
+        raise TypeError("q, block_table, seq_lens, out and workspace must be torch.Tensors")
+    _need_here((q, "q", torch.bfloat16, 3), (out, "out", torch.bfloat16, 3),
+               (block_table, "block_table", torch.int32, 2), (seq_lens, "seq_lens", torch.int32, 1),
+               (workspace, "workspace", torch.uint8, 1))
+    shape = q.shape
+    S, hq, d = shape
+    if d != desc.head_dim or out.shape != shape:
         raise ValueError(f"q and out must be [S][Hq][{desc.head_dim}] matching the cache")
     if block_table.shape[0] != S or seq_lens.shape[0] != S:
         raise ValueError("block_table and seq_lens need one row per sequence")
@@ -823,8 +861,7 @@ def saw_paged_decode_attn_prefix(q, kv_pages, scales, prefix_table, prefix_len, 
     desc = _cache_checks(kv_pages, scales, dev_status)
     S, hq = _decode_bf16_out_checks(q, block_table, seq_lens, out, workspace, desc)
     prefix_len = int(prefix_len)
-    if prefix_table is not None:
-        _need(prefix_table, "prefix_table", torch.int32, 1)
+    _need_here((prefix_table, "prefix_table", torch.int32, 1))
     if prefix_len > PAGE_SIZE * (0 if prefix_table is None else prefix_table.shape[0]):
         raise ValueError("prefix_table must hold a page for every 16 prefix tokens")
     if sm_scale is None:
@@ -881,11 +918,11 @@ def saw_evict_paged(kv_pages, scales, mass, block_table, seq_lens, new_table, ne
     if mass is None:
         raise TypeError("mass must be a torch.Tensor")
     desc = _cache_checks(kv_pages, scales, dev_status, mass)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    _need(new_table, "new_table", torch.int32, 2)
-    _need(new_lens, "new_lens", torch.int32, 1)
-    _need(kept, "kept", torch.int32, 3)
+    if any(t is None for t in (block_table, seq_lens, new_table, new_lens, kept)):
+        raise TypeError("block_table, seq_lens, new_table, new_lens and kept must be torch.Tensors")
+    _need_here((block_table, "block_table", torch.int32, 2), (seq_lens, "seq_lens", torch.int32, 1),
+               (new_table, "new_table", torch.int32, 2), (new_lens, "new_lens", torch.int32, 1),
+               (kept, "kept", torch.int32, 3))
     S = seq_lens.shape[0]
     if block_table.shape[0] != S or new_table.shape[0] != S or new_lens.shape[0] != S:
         raise ValueError("block_table, new_table and new_lens need one row per sequence")
