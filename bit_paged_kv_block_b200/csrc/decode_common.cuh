@@ -147,6 +147,7 @@ struct SeqTables {
 constexpr int kModeDecode = 0;
 constexpr int kModePrefill = 1;
 constexpr int kModePrefix = 2;
+constexpr int kMinSlice = 4;   // Plan::init's min_slice of a shared-prefix decode
 
 // Query tokens of sequence s (decode: 1) and its first query row; the decode instantiation has
 // none of the per-row arithmetic.
@@ -255,13 +256,15 @@ struct Plan {
     int64_t W;    // warps with a slice
     int64_t q, r;
 
-    __device__ void init(const SeqTables &tb_, int S_, int total_warps)
+    // min_slice: the least cost worth a warp of its own, where pieces are cheaper to attend over
+    // than to merge (1: every warp gets a slice)
+    __device__ void init(const SeqTables &tb_, int S_, int total_warps, int min_slice = 1)
     {
         tb = tb_;
         S = S_;
         P = tb.fpre[S];
         PT = P + kKappa * tb.spre[S];
-        W = max(int64_t(1), min(static_cast<int64_t>(total_warps), PT));
+        W = max(int64_t(1), min(static_cast<int64_t>(total_warps), PT / min_slice));
         q = PT / W;
         r = PT - q * W;
     }
@@ -733,7 +736,7 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
         return;
     }
     Plan plan;
-    plan.init(tb, S, p.total_warps);
+    plan.init(tb, S, p.total_warps, kMode == kModePrefix ? kMinSlice : 1);
     const int64_t u = static_cast<int64_t>(blockIdx.x) * Fmt::kWarps + warp;
     int64_t F0, F1;
     if (p.win_part == 1) {
@@ -963,12 +966,8 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
 
         Fmt::piece_end(st);
         if constexpr (kMode == kModePrefix) {
-            // every piece goes to its slot; the prefix's pieces as rows, for the merge kernel
-            float *slot = p.partials + (tb.spre[cs] + cj + u) * slot_floats<Fmt::kTiles>();
-            if (cs == p.prefix_seq)
-                store_partial_rows(slot, lane, st);
-            else
-                store_partial(slot, lane, st);
+            // every piece goes to its slot as rows, for the merge kernel
+            store_partial_rows(p.partials + (tb.spre[cs] + cj + u) * slot_floats<Fmt::kTiles>(), lane, st);
         } else if (seg_start >= F0 && ends_segment) {
             Segment<kMode> sg;
             sg.init(p, tb, cs, cj);

@@ -358,8 +358,7 @@ __device__ __forceinline__ void store_bf16_row(uint16_t *dst, int g, const float
 // this thread holds; H acts on each block of min(kD, 128) elements of d.  As the quantized part
 // of a windowed decode, out instead becomes the softmax-weighted merge of this result and the
 // window part's row already in out: weights 2^lse / (2^lse_q + 2^lse_w), lse_q = m + log2 l.
-// (The decode with accumulated weights and the shared-prefix decode write bf16 rows instead, the
-// former with lse[row] = m + log2 l; a row that attended over nothing, l = 0, is zero.)
+// (The decode with accumulated weights writes bf16 rows and lse[row] = m + log2 l instead.)
 template <bool kRotate, int kD, int kRole, class Seg>
 __device__ __forceinline__ void finalize(const DecodeParams &p, const Seg &sg, int lane,
                                          float o[kD / 16][4], const float m[2], const float l[2])
@@ -367,9 +366,7 @@ __device__ __forceinline__ void finalize(const DecodeParams &p, const Seg &sg, i
     constexpr int kC = kD / 32;   // 32-element chunks of d
     constexpr bool kMerge = kRole == kRoleWindow;
     const int g = lane >> 2, t = lane & 3;
-    constexpr bool kBf16 = kRole == kRoleMass || kRole == kRolePrefix;
-    const float inv[2] = {kBf16 && l[0] == 0.0f ? 0.0f : 1.0f / l[0],
-                          kBf16 && l[1] == 0.0f ? 0.0f : 1.0f / l[1]};
+    const float inv[2] = {1.0f / l[0], 1.0f / l[1]};
     // v[e][c][j]: head 2t + e, d = 32c + 4g + j
     float v[2][kC][4];
 #pragma unroll
@@ -426,9 +423,9 @@ __device__ __forceinline__ void finalize(const DecodeParams &p, const Seg &sg, i
         if (head < sg.nrows) {
             const int64_t off = sg.row_offset(p, head, kD);
             float f = kRotate ? hadamard_c(kD) : 1.0f, fw = 0.0f;
-            if constexpr (kBf16) {
+            if constexpr (kRole == kRoleMass) {
                 store_bf16_row<kD>(p.out_bf16 + off, g, v[e], f);
-                if (kRole == kRoleMass && g == 0)
+                if (g == 0)
                     p.lse[off / kD] = m[e] + log2f(l[e]);
                 continue;
             }

@@ -10,8 +10,8 @@
 //
 // The decode kernel (decode_common.cuh, kModePrefix) takes the batch's own tokens and the prefix in
 // one plan: kv head h of the prefix has S G query rows in blocks of 8, each block a segment over the
-// prefix's pages.  All pieces go to workspace slots; the prefix's are stored as rows, since the rows
-// of an output segment (sequence, kv head, up to 8 heads) may lie in two of its blocks.
+// prefix's pages.  All pieces go to workspace slots as rows ([8][D] fp32, then m[8] and l[8]), since
+// the rows of an output segment (sequence, kv head, up to 8 heads) may lie in two blocks of the prefix.
 //
 // At D = 128 and from kTensorRows query rows per kv head on, the prefix is instead a kernel of its own on
 // the 5th-generation tensor cores (prefix_tc.cu), which the decode kernel over the own tokens runs
@@ -40,108 +40,159 @@ struct PrefixPieces {
     int32_t row_blocks, splits;
 };
 
-// One CTA per output segment (sequence s, kv head h, block of up to 8 of its heads): fold the pieces
-// of the sequence's own tokens, then those of the prefix for the same query rows, and write the rows.
-// The warps take pieces in turn and warp 0 folds the warps' results in order, so the result does not
-// depend on timing.
-template <bool kRotate, int kD>
-__global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const DecodeParams p, const PrefixPieces pre)
-{
-    using Fmt = PrefixFormat<kRotate, kD>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 15) & ~uintptr_t(15));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kTiles = Fmt::kTiles;
-    constexpr int kSlot = slot_floats<kTiles>();
-    SeqTables tb;
-    tb.bind(smem + merge_smem_tables<kTiles>(), p.num_seqs);
-    volatile int64_t *flags = reinterpret_cast<volatile int64_t *>(smem + merge_smem_flags<kTiles>());
-    float *slots = reinterpret_cast<float *>(smem);
+constexpr int kRowWarps = 4;
 
+// One output row's elements of a lane: D / 32 of them, in runs of at most 4 (d = 4 lane + j in each
+// 128-block; for D = 64 d = 2 lane + j).
+template <int kD>
+struct RowVec {
+    static constexpr int kRuns = kD == 256 ? 2 : 1, kRun = kD == 64 ? 2 : 4;
+    float v[kRuns][kRun];
+
+    __device__ void fma_row(const float *row, int lane, float w)
+    {
+#pragma unroll
+        for (int b = 0; b < kRuns; b++) {
+            if constexpr (kRun == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(row + 128 * b + 4 * lane);
+                v[b][0] = fmaf(w, x.x, v[b][0]);
+                v[b][1] = fmaf(w, x.y, v[b][1]);
+                v[b][2] = fmaf(w, x.z, v[b][2]);
+                v[b][3] = fmaf(w, x.w, v[b][3]);
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(row + 2 * lane);
+                v[b][0] = fmaf(w, x.x, v[b][0]);
+                v[b][1] = fmaf(w, x.y, v[b][1]);
+            }
+        }
+    }
+    // the unnormalised Hadamard transform of each block: the run in registers, the rest across lanes
+    __device__ void hadamard(int lane)
+    {
+#pragma unroll
+        for (int b = 0; b < kRuns; b++) {
+#pragma unroll
+            for (int hb = 1; hb < kRun; hb <<= 1)
+#pragma unroll
+                for (int j = 0; j < kRun; j++)
+                    if ((j & hb) == 0) {
+                        const float x = v[b][j], y = v[b][j + hb];
+                        v[b][j] = x + y;
+                        v[b][j + hb] = x - y;
+                    }
+#pragma unroll
+            for (int lb = 1; lb < 32; lb <<= 1) {
+#pragma unroll
+                for (int j = 0; j < kRun; j++) {
+                    const float o = __shfl_xor_sync(0xFFFFFFFFu, v[b][j], lb);
+                    v[b][j] = (lane & lb) ? o - v[b][j] : v[b][j] + o;
+                }
+            }
+        }
+    }
+    __device__ void store(uint16_t *row, int lane, float f) const
+    {
+#pragma unroll
+        for (int b = 0; b < kRuns; b++) {
+            if constexpr (kRun == 4)
+                *reinterpret_cast<uint2 *>(row + 128 * b + 4 * lane) =
+                    make_uint2(bf16x2_as_u32(v[b][0] * f, v[b][1] * f), bf16x2_as_u32(v[b][2] * f, v[b][3] * f));
+            else
+                *reinterpret_cast<uint32_t *>(row + 2 * lane) = bf16x2_as_u32(v[b][0] * f, v[b][1] * f);
+        }
+    }
+};
+
+// The rows of a piece: slot k of a row's list is base + k slots, at row `row` of 8.
+struct RowPieces {
+    const float *base;
+    int count, row;
+};
+
+// One CTA per output segment (sequence s, kv head h, block of up to 8 of its heads), one warp per row:
+// the row's pieces (those of its own tokens, then the prefix's) are joined with weights 2^(m_k - M),
+// which the lanes form for 32 pieces at once, so that the loads of the pieces' rows depend on nothing
+// but the list.  Pieces are taken in a fixed order: the result does not depend on timing.  (Folding one
+// piece after another, each waiting for the one before, took 16 us for 17 splits.)
+template <bool kRotate, int kD>
+__global__ void __launch_bounds__(32 * kRowWarps) prefix_merge_kernel(const DecodeParams p, const PrefixPieces pre)
+{
+    constexpr int kSlot = slot_floats<kD / 16>();
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int64_t *flags = reinterpret_cast<volatile int64_t *>(smem);
+    SeqTables tb;
+    tb.bind(smem + 16 * kRowWarps, p.num_seqs);
     scan_sequences<kModePrefix>(p, tb, flags, false);
     Plan plan;
-    plan.init(tb, p.num_seqs, p.total_warps);
-    pdl_wait();   // the pieces
+    plan.init(tb, p.num_seqs, p.total_warps, kMinSlice);
+    // the pieces of segment j of sequence s in the plan
+    auto planned = [&](int s, int j, int row) -> RowPieces {
+        const int64_t u_lo = plan.warp_of_cost(plan.page_cost(s, j, 0));
+        const int64_t u_hi = plan.warp_of_cost(plan.page_cost(s, j, tb.npg[s] - 1));
+        return {p.partials + (tb.spre[s] + j + u_lo) * kSlot, static_cast<int>(u_hi - u_lo) + 1, row};
+    };
+    pdl_wait();
     const int nb = (p.group + kRowsPerBlock - 1) / kRowsPerBlock;
-    const int g = lane >> 2, t = lane & 3;
     for (int o = blockIdx.x; o < p.batch * p.hkv * nb; o += gridDim.x) {
         const int s = o / (p.hkv * nb), j = o - s * (p.hkv * nb);
+        const int h = j / nb, row0 = kRowsPerBlock * (j - h * nb), nrows = min(kRowsPerBlock, p.group - row0);
         const int len = p.seq_lens[s];
         const bool valid = len >= 0 && len <= p.max_blocks * kPageSize;
-        WarpState<kTiles> st;
-        state_reset(st);
-        if (valid && tb.npg[s] > 0) {
-            const int64_t gseg = tb.spre[s] + j;
-            const int64_t u_hi = plan.warp_of_cost(plan.page_cost(s, j, tb.npg[s] - 1));
-            for (int64_t u = plan.warp_of_cost(plan.page_cost(s, j, 0)) + warp; u <= u_hi; u += kMergeWarps) {
-                float bm[2], bl[2];
-                float4 bo[kTiles];
-                load_partial(p.partials + (gseg + u) * kSlot, lane, bm, bl, bo);
-                merge_into(st.m, st.l, st.o, bm, bl, bo);
-            }
-        }
-        Segment<kModePrefix> sg;
-        sg.s = s;
-        sg.j = j;
-        sg.h = j / nb;
-        sg.b = j - sg.h * nb;
-        sg.row0 = kRowsPerBlock * sg.b;
-        sg.nrows = min(kRowsPerBlock, p.group - sg.row0);
-        sg.qrow0 = s;
-        if (valid && (p.prefix_seq >= 0 || pre.splits > 0)) {
-            const int ps = p.prefix_seq;
+        RowPieces own = {nullptr, 0, 0};
+        if (valid && tb.npg[s] > 0)
+            own = planned(s, j, 0);
+        for (int e = warp; e < nrows; e += kRowWarps) {
+            RowPieces part[2] = {own, {nullptr, 0, 0}};
+            part[0].row = e;
+            const int row = s * p.group + row0 + e;   // the prefix's row of this head
+            if (valid && pre.splits > 0)
+                part[1] = {pre.slots + (static_cast<int64_t>(h) * pre.row_blocks + row / kRowsPerBlock) * pre.splits * kSlot,
+                           pre.splits, row % kRowsPerBlock};
+            else if (valid && p.prefix_seq >= 0)
+                part[1] = planned(p.prefix_seq, h * tb.nbk[p.prefix_seq] + row / kRowsPerBlock, row % kRowsPerBlock);
+            RowVec<kD> acc = {};
+            float M = -INFINITY, l = 0.0f;   // l: this lane's share
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
-                if (2 * t + e >= sg.nrows)
-                    continue;
-                const int row = s * p.group + sg.row0 + 2 * t + e;
-                const int pr = row % kRowsPerBlock;
-                const float *slot0;
-                int pieces;
-                if (pre.splits > 0) {
-                    slot0 = pre.slots + (static_cast<int64_t>(sg.h) * pre.row_blocks + row / kRowsPerBlock) * pre.splits * kSlot;
-                    pieces = pre.splits;
-                } else {
-                    const int pj = sg.h * tb.nbk[ps] + row / kRowsPerBlock;
-                    const int64_t u_lo = plan.warp_of_cost(plan.page_cost(ps, pj, 0));
-                    slot0 = p.partials + (tb.spre[ps] + pj + u_lo) * kSlot;
-                    pieces = static_cast<int>(plan.warp_of_cost(plan.page_cost(ps, pj, tb.npg[ps] - 1)) - u_lo) + 1;
-                }
-                for (int k = warp; k < pieces; k += kMergeWarps) {
-                    const float *slot = slot0 + static_cast<int64_t>(k) * kSlot;
-                    const float bm = slot[8 * kD + pr], bl = slot[8 * kD + 8 + pr];
-                    const float4 *o4 = reinterpret_cast<const float4 *>(slot + pr * kD) + g;
-                    const float mn = fmaxf(st.m[e], bm);
-                    const float fa = mn == -INFINITY ? 0.0f : ex2_approx(st.m[e] - mn);
-                    const float fb = mn == -INFINITY ? 0.0f : ex2_approx(bm - mn);
-                    st.m[e] = mn;
-                    st.l[e] = st.l[e] * fa + bl * fb;
+            for (int q = 0; q < 2; q++) {
+                for (int k0 = 0; k0 < part[q].count; k0 += 32) {
+                    const int n = min(32, part[q].count - k0);
+                    const float *slot = part[q].base + static_cast<int64_t>(k0) * kSlot;
+                    const float mk = lane < n ? slot[static_cast<int64_t>(lane) * kSlot + 8 * kD + part[q].row] : -INFINITY;
+                    const float lk = lane < n ? slot[static_cast<int64_t>(lane) * kSlot + 8 * kD + 8 + part[q].row] : 0.0f;
+                    float top = mk;
 #pragma unroll
-                    for (int c = 0; c < kTiles / 2; c++) {
-                        const float4 v = o4[8 * c];
-                        st.o[2 * c][e] = st.o[2 * c][e] * fa + v.x * fb;
-                        st.o[2 * c][2 + e] = st.o[2 * c][2 + e] * fa + v.y * fb;
-                        st.o[2 * c + 1][e] = st.o[2 * c + 1][e] * fa + v.z * fb;
-                        st.o[2 * c + 1][2 + e] = st.o[2 * c + 1][2 + e] * fa + v.w * fb;
-                    }
+                    for (int d = 1; d < 32; d <<= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                    top = fmaxf(top, M);
+                    const float old = M == -INFINITY ? 0.0f : ex2_approx(M - top);
+                    const float w = mk == -INFINITY ? 0.0f : ex2_approx(mk - top);
+                    M = top;
+                    l = l * old + lk * w;
+#pragma unroll
+                    for (int b = 0; b < RowVec<kD>::kRuns; b++)
+#pragma unroll
+                        for (int i = 0; i < RowVec<kD>::kRun; i++)
+                            acc.v[b][i] *= old;
+                    const float *r = slot + part[q].row * kD;
+#pragma unroll 8
+                    for (int k = 0; k < n; k++)
+                        acc.fma_row(r + static_cast<int64_t>(k) * kSlot, lane, __shfl_sync(0xFFFFFFFFu, w, k));
                 }
             }
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1)
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+            if (kRotate)
+                acc.hadamard(lane);
+            // a row that attended over nothing is zero
+            const float f = l == 0.0f ? 0.0f : (kRotate ? hadamard_c(kD) : 1.0f) / l;
+            acc.store(p.out_bf16 + (static_cast<int64_t>(s) * p.hq + h * p.group + row0 + e) * kD, lane, f);
         }
-        if (warp > 0)
-            store_partial(slots + (warp - 1) * kSlot, lane, st);
-        __syncthreads();
-        if (warp == 0) {
-            for (int w = 1; w < kMergeWarps; w++) {
-                float bm[2], bl[2];
-                float4 bo[kTiles];
-                load_partial(slots + (w - 1) * kSlot, lane, bm, bl, bo);
-                merge_into(st.m, st.l, st.o, bm, bl, bo);
-            }
-            Fmt::finalize(p, sg, lane, st.o, st.m, st.l);
-        }
-        __syncthreads();
     }
 }
+
+inline size_t row_merge_smem(int32_t num_seqs) { return 16 * kRowWarps + seq_table_bytes(num_seqs); }
 
 template <int kD>
 cudaError_t prefix_shape(size_t smem, size_t merge_smem, LaunchShape &out)
@@ -184,7 +235,7 @@ cudaError_t prefix_plan(int32_t hkv, int32_t hq, int32_t num_seqs, int32_t prefi
     pl.tensor = kD == 128 && prefix_len > 0 && rows >= kTensorRows;
     pl.plan_seqs = num_seqs + (prefix_len > 0 && !pl.tensor ? 1 : 0);
     pl.smem = decode_smem_bytes<Fmt>(pl.plan_seqs, kRowsPerBlock);
-    pl.merge_smem = merge_smem_bytes<Fmt::kTiles>(pl.plan_seqs);
+    pl.merge_smem = row_merge_smem(pl.plan_seqs);
     const cudaError_t e = prefix_shape<kD>(pl.smem, pl.merge_smem, pl.ls);
     if (e != cudaSuccess)
         return e;
@@ -243,8 +294,8 @@ cudaError_t launch(const DecodeArgs &a, const int32_t *prefix_table, int32_t pre
     if (e != cudaSuccess)
         return e;
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(max_segments(a.num_kv_heads, a.num_q_heads, a.num_seqs, 0, false),
-                                                               8 * pl.ls.sms)));
-    cfg.blockDim = dim3(kMergeThreads);
+                                                               16 * pl.ls.sms)));
+    cfg.blockDim = dim3(32 * kRowWarps);
     cfg.dynamicSmemBytes = pl.merge_smem;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, prefix_merge_kernel<kRotate, kD>, p, pre);

@@ -40,8 +40,8 @@ constexpr int kTok = 128;                    // tokens of a block
 constexpr int kHalfTile = kTok * 128;        // bytes of one 64-wide half (128 B rows) of a tile
 constexpr float kHadC = 0.0883883461356163f;
 constexpr float kQLift = 16.0f;              // query entries enter scaled by 2^4, clear of subnormals
-constexpr float kLag = 4.0f;                 // log2: how far a row may exceed its reference maximum
-constexpr float kLift = 11.0f;
+constexpr float kLag = 6.0f;                 // log2: how far a row may exceed its reference maximum
+constexpr float kLift = 9.0f;
 
 // shared memory (from a 1024-byte aligned base)
 constexpr int kPtQ = 0;                               // 2 tiles x 2 halves x [128 rows][128 B]
@@ -51,14 +51,29 @@ constexpr int kPtBars = kPtV + 2 * 2 * kHalfTile;     // 15 mbarriers, tensor-me
 constexpr int kPtBytes = kPtBars + 256;
 constexpr size_t kPtSmem = 1024 + kPtBytes;
 
-// A from tensor memory: D[d] (+)= A[a] B[b]
-__device__ __forceinline__ void umma_f16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate)
+// One elected lane of a converged warp issues a product D[d] (+)= A B, A from shared memory or (_ta) from
+// tensor memory, or a commit.  The whole warp runs the issuing loop, so that the operands are
+// warp-uniform: from one diverged lane, moving them to the uniform registers that these instructions
+// take cost 100 cycles a product, as long as the product itself.
+__device__ __forceinline__ void umma_elected(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(tmem_d), "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate)
+    asm volatile("{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
                  : "memory");
+}
+__device__ __forceinline__ void umma_elected_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                 ::"r"(bar) : "memory");
 }
 
 // 32 columns of this thread's tensor-memory lane, queued; tmem_wait makes them readable
@@ -85,6 +100,11 @@ __device__ __forceinline__ void tmem_wait(uint32_t r[32])
                  :
                  : "memory");
 }
+__device__ __forceinline__ void tmem_wait2(uint32_t r[32], uint32_t q[32])
+{
+    tmem_wait(r);
+    tmem_wait(q);
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t r[32])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
@@ -105,6 +125,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t r[16])
                    "r"(r[15])
                  : "memory");
 }
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // The 8 codes of a word as zero + code scale, in the pair order (d, d + 4), (d + 1, d + 5), ...: a
@@ -124,6 +148,12 @@ __device__ __forceinline__ void dequant_word_store(uint32_t dst, uint32_t w, __h
                  : "memory");
 }
 
+// 16 bytes global -> shared without a register on the way, or zeros
+__device__ __forceinline__ void copy16_zfill(uint32_t dst, const void *src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
 struct PrefixTcParams {
     const uint16_t *q;           // bf16 [S][Hq][128]
     const uint8_t *codes;
@@ -137,6 +167,72 @@ struct PrefixTcParams {
     int32_t row_pairs;           // pairs of row tiles per kv head
     int32_t splits, split_blocks;
     float q_mult;
+};
+
+// One producer thread's share of a block: 4 rows (tokens) x one 16-byte quarter of their K and V code
+// rows, and the rows' (scale, zero) pairs.
+struct Words {
+    uint4 k[4], v[4];
+    uint32_t sk[4], sv[4];
+};
+struct Producer {
+    int h, first, rk, q4, pg, n_pages;
+    int32_t id[4];
+    Words cur;
+
+    // Lane -> (row of 8, 16-byte quarter of the 64-byte code row) such that the 8 lanes of a store
+    // phase (4 rows x 2 adjacent quarters) hit 8 different 16-byte columns of the swizzled tile.
+    __device__ void init(const PrefixTcParams &p, int h_, int first_, int pw, int lane)
+    {
+        h = h_;
+        first = first_;
+        q4 = (lane & 1) | (((lane >> 3) & 1) << 1);
+        rk = 8 * (pw & 1) + (((lane >> 1) & 3) | ((lane >> 4) << 2));   // token within its page
+        pg = pw >> 1;                                                    // pages pg + 2 i of a block
+        n_pages = (p.len + kPageSize - 1) / kPageSize;
+    }
+    // page ids of block b
+    __device__ void ids(const PrefixTcParams &p, int b)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int j = first / kPageSize + 8 * b + pg + 2 * i;
+            id[i] = j < n_pages ? __ldg(p.table + j) : 0;
+            if (id[i] < 0 || id[i] >= p.num_pages) {
+                set_status(p.status, SAW_DEV_BAD_PAGE);
+                id[i] = 0;
+            }
+        }
+    }
+    // the words of block b, whose ids have been read
+    __device__ void fetch(const PrefixTcParams &p, int b, Words &w) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int64_t at = static_cast<int64_t>(id[i]) * p.hkv + h;
+            const uint8_t *c = p.codes + at * 2048 + rk * 64 + q4 * 16;
+            const uint8_t *s = p.scales + at * 128 + rk * 4;
+            w.k[i] = ldg_nc16(c);
+            w.v[i] = ldg_nc16(c + 1024);
+            // tokens past the prefix: scale and zero 0, so K^ and V^ are 0 whatever the rows hold
+            const bool in = first + kTok * b + kPageSize * (pg + 2 * i) + rk < p.len;
+            w.sk[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(s)) : 0u;
+            w.sv[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(s + 64)) : 0u;
+        }
+    }
+    __device__ void unpack(uint32_t tile, const uint4 w[4], const uint32_t sz[4]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int row = kPageSize * (pg + 2 * i) + rk;
+            const __half2 scale = u32_as_half2(__byte_perm(sz[i], 0, 0x1010));
+            const __half2 zero = u32_as_half2(__byte_perm(sz[i], 0, 0x3232));
+            dequant_word_store(tile + sw128_chunk(row, 4 * q4 + 0, kHalfTile), w[i].x, scale, zero);
+            dequant_word_store(tile + sw128_chunk(row, 4 * q4 + 1, kHalfTile), w[i].y, scale, zero);
+            dequant_word_store(tile + sw128_chunk(row, 4 * q4 + 2, kHalfTile), w[i].z, scale, zero);
+            dequant_word_store(tile + sw128_chunk(row, 4 * q4 + 3, kHalfTile), w[i].w, scale, zero);
+        }
+    }
 };
 
 template <bool kRotate>
@@ -189,192 +285,147 @@ __global__ void __launch_bounds__(kPtThreads, 1) prefix_tc_kernel(const PrefixTc
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
 
-    // ---- the query tiles: rotate, scale, fp16, in the codes' d order (a thread per row) -----------
+    // ---- the raw query tiles and the rotation matrix ----------------------------------------------
+    // Raw bf16 rows by coalesced 16-byte loads (16 lanes a row) into the tile they end up in; and, into
+    // the V stage that is filled last, the matrix whose product with them is the rotated query in the
+    // codes' d order: row n holds the signs of the Hadamard matrix's row d_n (for a plain cache, a 1 at
+    // d_n).  One bf16 product per tile, exact up to fp32 addition, replaces 7 butterfly stages of
+    // straight-line code: code that runs once costs its instruction fetches, 10 cycles each.
+    Producer pr;
+    if (warp >= 8 && warp < 12) {   // the first block's words are on their way meanwhile
+        pr.init(p, h, first, warp - 8, lane);
+        pr.ids(p, 0);
+        pr.fetch(p, 0, pr.cur);
+        if (nb > 1)
+            pr.ids(p, 1);
+    }
     if (warp < 8) {
-        const int r = row0 + tid;
-        const bool live = r < p.rows;
-        const int seq = live ? r / p.group : 0, head = live ? r - seq * p.group : 0;
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.q + (static_cast<int64_t>(seq) * p.hq + h * p.group + head) * 128);
-#pragma unroll 1
-        for (int hf = 0; hf < 2; hf++) {
-            float x[64];
-#pragma unroll
-            for (int c = 0; c < 8; c++) {
-                const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
-                const uint4 ua = live ? src[c] : zero4, ub = live ? src[8 + c] : zero4;
-                const uint32_t wa[4] = {ua.x, ua.y, ua.z, ua.w}, wb[4] = {ub.x, ub.y, ub.z, ub.w};
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const float a = __uint_as_float(e ? (wa[k] & 0xFFFF0000u) : (wa[k] << 16));
-                        const float b = __uint_as_float(e ? (wb[k] & 0xFFFF0000u) : (wb[k] << 16));
-                        x[8 * c + 2 * k + e] = !kRotate ? (hf ? b : a) : (hf ? a - b : a + b);
-                    }
-            }
-#pragma unroll
-            for (int hb = 1; kRotate && hb < 64; hb <<= 1)
-#pragma unroll
-                for (int i = 0; i < 64; i++)
-                    if ((i & hb) == 0) {
-                        const float a = x[i], b = x[i + hb];
-                        x[i] = a + b;
-                        x[i + hb] = a - b;
-                    }
-            const uint32_t tile = sbase + kPtQ + (tid >> 7) * 2 * kHalfTile;
-#pragma unroll
-            for (int c = 0; c < 8; c++) {
-                uint32_t wv[4];
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-                    wv[k] = half2_as_u32(__floats2half2_rn(x[8 * c + chunk_d(2 * k)] * (p.q_mult * kQLift),
-                                                           x[8 * c + chunk_d(2 * k + 1)] * (p.q_mult * kQLift)));
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile + sw128_chunk(tid & 127, 8 * hf + c, kHalfTile)),
-                             "r"(wv[0]), "r"(wv[1]), "r"(wv[2]), "r"(wv[3]) : "memory");
-            }
+#pragma unroll 2
+        for (int i = tid; i < tiles * kRows * 16; i += 256) {
+            const int row = i >> 4, c = i & 15, r = row0 + row;
+            const int seq = r / p.group, head = r - seq * p.group;
+            const uint16_t *src = p.q + (static_cast<int64_t>(seq) * p.hq + h * p.group + head) * 128 + 8 * c;
+            copy16_zfill(sbase + kPtQ + (row >> 7) * 2 * kHalfTile + sw128_chunk(row & 127, c, kHalfTile),
+                         r < p.rows ? src : p.q, r < p.rows);
         }
-        async_proxy_fence();   // the tile is read by the tensor cores
+#pragma unroll 1
+        for (int i = tid; i < 128 * 16; i += 256) {
+            const int n = i >> 4, c = i & 15, dn = (n & ~7) + chunk_d(n & 7);
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const int d = 8 * c + 2 * k;
+                if (kRotate)   // +-1 in bf16
+                    w[k] = 0x3F803F80u | (static_cast<uint32_t>(__popc(dn & d) & 1) << 15) |
+                           (static_cast<uint32_t>(__popc(dn & (d + 1)) & 1) << 31);
+                else
+                    w[k] = (dn == d ? 0x3F80u : 0u) | (dn == d + 1 ? 0x3F800000u : 0u);
+            }
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                         ::"r"(sbase + kPtV + 2 * kHalfTile + sw128_chunk(n, c, kHalfTile)), "r"(w[0]), "r"(w[1]),
+                         "r"(w[2]), "r"(w[3]) : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        async_proxy_fence();   // both are read by the tensor cores
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t tmem = 0;   // all 512 columns are this CTA's
     auto o_col = [&](int t) { return tmem + 128u * t; };
     auto s_col = [&](int t) { return tmem + 256u + 128u * t; };
 
     if (warp >= 8 && warp < 12) {
         // ======== producers ==========================================================================
-        // Lane -> (row of 8, 16-byte quarter of the 64-byte code row) such that the 8 lanes of a store
-        // phase (4 rows x 2 adjacent quarters) hit 8 different 16-byte columns of the swizzled tile.
-        const int pw = warp - 8;
-        const int q4 = (lane & 1) | (((lane >> 3) & 1) << 1);
-        const int r8 = ((lane >> 1) & 3) | ((lane >> 4) << 2);
-        const int rk = 8 * (pw & 1) + r8;          // token within its page
-        const int pg = pw >> 1;                    // pages pg + 2 i of a block
-        const int n_pages = (p.len + kPageSize - 1) / kPageSize, page0 = first / kPageSize;
-        struct Words {
-            uint4 k[4], v[4];
-            uint32_t sk[4], sv[4];
-        };
-        auto ids = [&](int b, int32_t id[4]) {
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int j = page0 + 8 * b + pg + 2 * i;
-                id[i] = j < n_pages ? __ldg(p.table + j) : -1;
-                if (j < n_pages && (id[i] < 0 || id[i] >= p.num_pages)) {
-                    set_status(p.status, SAW_DEV_BAD_PAGE);
-                    id[i] = 0;
-                }
-            }
-        };
-        auto fetch = [&](int b, const int32_t id[4], Words &w) {
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int64_t at = static_cast<int64_t>(max(id[i], 0)) * p.hkv + h;
-                const uint8_t *c = p.codes + at * 2048 + rk * 64 + q4 * 16;
-                const uint8_t *s = p.scales + at * 128 + rk * 4;
-                w.k[i] = ldg_nc16(c);
-                w.v[i] = ldg_nc16(c + 1024);
-                // tokens past the prefix: scale and zero 0, so K^ and V^ are 0 whatever the rows hold
-                const bool in = first + kTok * b + kPageSize * (pg + 2 * i) + rk < p.len;
-                w.sk[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(s)) : 0u;
-                w.sv[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(s + 64)) : 0u;
-            }
-        };
-        auto unpack = [&](uint32_t tile, const uint4 w[4], const uint32_t sz[4]) {
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int row = kPageSize * (pg + 2 * i) + rk;
-                const __half2 scale = u32_as_half2(__byte_perm(sz[i], 0, 0x1010));
-                const __half2 zero = u32_as_half2(__byte_perm(sz[i], 0, 0x3232));
-                dequant_word_store(tile + sw128_chunk(row, 4 * q4 + 0, kHalfTile), w[i].x, scale, zero);
-                dequant_word_store(tile + sw128_chunk(row, 4 * q4 + 1, kHalfTile), w[i].y, scale, zero);
-                dequant_word_store(tile + sw128_chunk(row, 4 * q4 + 2, kHalfTile), w[i].z, scale, zero);
-                dequant_word_store(tile + sw128_chunk(row, 4 * q4 + 3, kHalfTile), w[i].w, scale, zero);
-            }
-        };
-        int32_t id[4];
-        Words cur, nxt;
-        ids(0, id);
-        fetch(0, id, cur);
-        if (nb > 1)
-            ids(1, id);
         for (int kb = 0; kb < nb; kb++) {
+            Words nxt;
             if (kb + 1 < nb)
-                fetch(kb + 1, id, nxt);
+                pr.fetch(p, kb + 1, nxt);
             if (kb + 2 < nb)
-                ids(kb + 2, id);
+                pr.ids(p, kb + 2);
             const int st = kb & 1;
             const uint32_t parity = static_cast<uint32_t>((kb - 2) >> 1) & 1u;
             if (kb >= 2 && !tc_wait(k_empty(st), parity, abort_flag))
                 break;
-            unpack(sbase + kPtK + st * 2 * kHalfTile, cur.k, cur.sk);
+            pr.unpack(sbase + kPtK + st * 2 * kHalfTile, pr.cur.k, pr.cur.sk);
             async_proxy_fence();
             tc_arrive(k_full(st));
-            if (kb >= 2 && !tc_wait(v_empty(st), parity, abort_flag))
+            // (the second V stage held the rotation matrix first)
+            if (kb >= 1 && !tc_wait(v_empty(st), static_cast<uint32_t>(st ? (kb - 1) >> 1 : (kb - 2) >> 1) & 1u, abort_flag))
                 break;
-            unpack(sbase + kPtV + st * 2 * kHalfTile, cur.v, cur.sv);
+            pr.unpack(sbase + kPtV + st * 2 * kHalfTile, pr.cur.v, pr.cur.sv);
             async_proxy_fence();
             tc_arrive(v_full(st));
-            cur = nxt;
+            pr.cur = nxt;
         }
     } else if (warp == 12) {
-        // ======== the products =========================================================================
-        if (lane == 0) {
-            constexpr uint32_t id_qk = umma_idesc(kRows, kTok, 0, 0);
-            constexpr uint32_t id_pv = umma_idesc(kRows, 128, 0, 1);
-            auto issue_qk = [&](int t, int kb) {
-                const uint32_t q = sbase + kPtQ + t * 2 * kHalfTile, k = sbase + kPtK + (kb & 1) * 2 * kHalfTile;
+        // ======== the products (the whole warp; one lane issues) =========================================
+        constexpr uint32_t id_qk = umma_idesc(kRows, kTok, 0, 0);
+        constexpr uint32_t id_pv = umma_idesc(kRows, 128, 0, 1);
+        constexpr uint32_t id_rot = umma_idesc(kRows, 128, 0, 0) | (1u << 7) | (1u << 10);   // bf16 operands
+        constexpr uint64_t kTile16 = 2 * kHalfTile / 16, kHalf16 = kHalfTile / 16;
+        const uint64_t dq = umma_desc(sbase + kPtQ, 16, 1024), dk = umma_desc(sbase + kPtK, 16, 1024);
+        const uint64_t dv = umma_desc(sbase + kPtV, kHalfTile, 1024);
+        const uint64_t dh = umma_desc(sbase + kPtV + 2 * kHalfTile, 16, 1024);
+        auto issue_ab = [&](int t, uint64_t a, uint64_t b, uint32_t idesc) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ks++) {
-                    const uint32_t off = (ks >> 2) * kHalfTile + (ks & 3) * 32;
-                    umma_f16(s_col(t), umma_desc(q + off, 16, 1024), umma_desc(k + off, 16, 1024), id_qk, ks > 0);
-                }
-                umma_commit(s_full(t));
-            };
-            auto issue_pv = [&](int t, int kb) {
-                const uint32_t v = sbase + kPtV + (kb & 1) * 2 * kHalfTile;
+            for (int ks = 0; ks < 8; ks++) {
+                const uint64_t off = (ks >> 2) * kHalf16 + (ks & 3) * 2;
+                umma_elected(s_col(t), a + off, b + off, idesc, ks > 0);
+            }
+            commit_elected(s_full(t));
+        };
+        auto issue_qk = [&](int t, int kb) { issue_ab(t, dq + t * kTile16, dk + (kb & 1) * kTile16, id_qk); };
+        auto issue_pv = [&](int t, int kb) {
+            const uint64_t v = dv + (kb & 1) * kTile16;
 #pragma unroll
-                for (int ks = 0; ks < 8; ks++)
-                    umma_f16_ta(o_col(t), s_col(t) + 8 * ks, umma_desc(v + ks * 2048, kHalfTile, 1024), id_pv,
-                                kb > 0 || ks > 0);
-                umma_commit(o_done(t));
-            };
-            bool ok = tc_wait(k_full(0), 0, abort_flag);
+            for (int ks = 0; ks < 8; ks++)
+                umma_elected_ta(o_col(t), s_col(t) + 8 * ks, v + ks * (2048 / 16), id_pv, kb > 0 || ks > 0);
+            commit_elected(o_done(t));
+        };
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xFFFFFFFFu, tc_wait(bar, parity, abort_flag));
+        };
+        for (int t = 0; t < tiles; t++)
+            issue_ab(t, dq + t * kTile16, dh, id_rot);   // the rotated queries, where the logits will be
+        commit_elected(v_empty(1));
+        // phase 0 of s_full / p_full is the rotation; block kb is phase kb + 1
+        bool ok = wait(k_full(0), 0);
+        for (int t = 0; ok && t < tiles; t++) {
+            ok = wait(p_full(t), 0);
             if (ok) {
                 tc_fence_after();
-                for (int t = 0; t < tiles; t++)
-                    issue_qk(t, 0);
-                umma_commit(k_empty(0));
+                issue_qk(t, 0);
             }
-            for (int kb = 0; ok && kb < nb; kb++) {
-                const uint32_t par = static_cast<uint32_t>(kb) & 1u, par2 = static_cast<uint32_t>(kb >> 1) & 1u;
-                for (int t = 0; ok && t < tiles; t++) {
-                    ok = (t > 0 || tc_wait(v_full(kb & 1), par2, abort_flag)) && tc_wait(p_full(t), par, abort_flag);
+        }
+        commit_elected(k_empty(0));
+        for (int kb = 0; ok && kb < nb; kb++) {
+            const uint32_t par = static_cast<uint32_t>(kb) & 1u, par2 = static_cast<uint32_t>(kb >> 1) & 1u;
+            ok = wait(v_full(kb & 1), par2);
+            for (int t = 0; ok && t < tiles; t++) {
+                ok = wait(p_full(t), par ^ 1u);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                issue_pv(t, kb);
+                if (t == tiles - 1)
+                    commit_elected(v_empty(kb & 1));
+                if (kb + 1 < nb) {
+                    // the next logits overwrite this block's weights: once P V has read them
+                    ok = (t > 0 || wait(k_full((kb + 1) & 1), static_cast<uint32_t>((kb + 1) >> 1) & 1u)) &&
+                         wait(o_done(t), par);
                     if (!ok)
                         break;
                     tc_fence_after();
-                    issue_pv(t, kb);
+                    issue_qk(t, kb + 1);
                     if (t == tiles - 1)
-                        umma_commit(v_empty(kb & 1));
-                    if (kb + 1 < nb) {
-                        // the next logits overwrite this block's weights: once P V has read them
-                        ok = (t > 0 || tc_wait(k_full((kb + 1) & 1), static_cast<uint32_t>((kb + 1) >> 1) & 1u, abort_flag)) &&
-                             tc_wait(o_done(t), par, abort_flag);
-                        if (!ok)
-                            break;
-                        tc_fence_after();
-                        issue_qk(t, kb + 1);
-                        if (t == tiles - 1)
-                            umma_commit(k_empty((kb + 1) & 1));
-                    }
+                        commit_elected(k_empty((kb + 1) & 1));
                 }
             }
-            // every product and its arrivals are over before shared and tensor memory are released
-            umma_commit(all_done);
-            mbar_wait_bounded(all_done, 0, kTcWaitLimitNs / 10);
         }
+        // every product and its arrivals are over before shared and tensor memory are released
+        commit_elected(all_done);
+        mbar_wait_bounded(all_done, 0, kTcWaitLimitNs / 10);
     } else if (warp < 8 && (warp >> 2) < tiles) {
         // ======== softmax: one row per thread ===========================================================
         const int t = warp >> 2;
@@ -383,36 +434,57 @@ __global__ void __launch_bounds__(kPtThreads, 1) prefix_tc_kernel(const PrefixTc
         const int r = row0 + tid;
         float m_ref = -INFINITY;
         uint64_t l2 = f2_pack(0.0f, 0.0f);
+        bool ok = __all_sync(0xFFFFFFFFu, tc_wait(s_full(t), 0, abort_flag));
+        if (ok) {
+            // the rotated query, scaled, as fp16 over the raw one
+            tc_fence_after();
+            const uint32_t tile = sbase + kPtQ + t * 2 * kHalfTile;
+            const float mul = p.q_mult * kQLift;
+#pragma unroll 1
+            for (int c = 0; c < 4; c++) {
+                uint32_t a[32];
+                tmem_ld32_async(so + 32 * c, a);
+                tmem_wait(a);
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    a[i] = half2_as_u32(__floats2half2_rn(__uint_as_float(a[2 * i]) * mul, __uint_as_float(a[2 * i + 1]) * mul));
+#pragma unroll
+                for (int g = 0; g < 4; g++)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                                 ::"r"(tile + sw128_chunk(tid & 127, 4 * c + g, kHalfTile)), "r"(a[4 * g]),
+                                 "r"(a[4 * g + 1]), "r"(a[4 * g + 2]), "r"(a[4 * g + 3]) : "memory");
+            }
+            async_proxy_fence();
+            tc_fence_before();
+            tc_arrive(p_full(t));
+        }
         const uint64_t unlift = f2_pack(1.0f / kQLift, 1.0f / kQLift);
-        bool ok = true;
-        for (int kb = 0; kb < nb; kb++) {
-            ok = tc_wait(s_full(t), static_cast<uint32_t>(kb) & 1u, abort_flag);
+        for (int kb = 0; ok && kb < nb; kb++) {
+            ok = tc_wait(s_full(t), static_cast<uint32_t>(kb + 1) & 1u, abort_flag);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok)
                 break;
             tc_fence_after();
-            const int valid = n_tok - kTok * kb;   // tokens of the block that exist (more: all)
+            // logits of tokens past the prefix (its last block)
+            for (int n = n_tok - kTok * kb; n < kTok; n++)
+                tmem_st1(so + n, __float_as_uint(-INFINITY));
+            if (n_tok - kTok * kb < kTok)
+                tmem_wait_st();
             uint32_t a[32], b[32];
             // the row's maximum
             float mx = -INFINITY;
-            tmem_ld32_async(so, a);
+#pragma unroll 1
+            for (int c = 0; c < 2; c++) {
+                tmem_ld32_async(so + 64 * c, a);
+                tmem_ld32_async(so + 64 * c + 32, b);
+                tmem_wait2(a, b);
+                float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < 4; c++) {
-                uint32_t *x = (c & 1) ? b : a;
-                tmem_wait(x);
-                if (c < 3)
-                    tmem_ld32_async(so + 32 * (c + 1), (c & 1) ? a : b);
-                if (valid < 32 * (c + 1)) {
-#pragma unroll
-                    for (int i = 0; i < 32; i++)
-                        mx = 32 * c + i < valid ? fmaxf(mx, __uint_as_float(x[i])) : mx;
-                } else {
-                    float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        m4[(i >> 1) & 3] = fmax3(m4[(i >> 1) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-                    mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+                for (int i = 0; i < 32; i += 2) {
+                    m4[(i >> 1) & 3] = fmax3(m4[(i >> 1) & 3], __uint_as_float(a[i]), __uint_as_float(a[i + 1]));
+                    m4[(i >> 1) & 3] = fmax3(m4[(i >> 1) & 3], __uint_as_float(b[i]), __uint_as_float(b[i + 1]));
                 }
+                mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
             }
             mx *= 1.0f / kQLift;
             const bool grow = mx > m_ref + kLag;
@@ -443,27 +515,27 @@ __global__ void __launch_bounds__(kPtThreads, 1) prefix_tc_kernel(const PrefixTc
             // 16 c .. 16 c + 15, whose logits have been read by then)
             const float shift = kLift - m_ref;
             const uint64_t sh2 = f2_pack(shift, shift);
-            tmem_ld32_async(so, a);
-#pragma unroll
-            for (int c = 0; c < 4; c++) {
-                uint32_t *x = (c & 1) ? b : a;
-                tmem_wait(x);
-                if (c < 3)
-                    tmem_ld32_async(so + 32 * (c + 1), (c & 1) ? a : b);
-                uint32_t w[16];
+            auto weigh = [&](uint32_t x[32], uint32_t to) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
                     float y0, y1;
                     f2_unpack(f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), unlift, sh2), y0, y1);
-                    float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
-                    if (valid < 32 * (c + 1)) {
-                        e0 = 32 * c + i < valid ? e0 : 0.0f;
-                        e1 = 32 * c + i + 1 < valid ? e1 : 0.0f;
-                    }
+                    const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
                     l2 = f2_add(l2, f2_pack(e0, e1));
-                    w[i >> 1] = half2_as_u32(__floats2half2_rn(e0, e1));
+                    x[i >> 1] = half2_as_u32(__floats2half2_rn(e0, e1));
                 }
-                tmem_st16(so + 16 * c, w);
+                tmem_st16(to, x);
+            };
+            tmem_ld32_async(so, a);
+#pragma unroll 1
+            for (int c = 0; c < 2; c++) {
+                tmem_wait(a);
+                tmem_ld32_async(so + 64 * c + 32, b);
+                weigh(a, so + 32 * c);
+                tmem_wait(b);
+                if (c == 0)
+                    tmem_ld32_async(so + 64, a);
+                weigh(b, so + 32 * c + 16);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -474,28 +546,46 @@ __global__ void __launch_bounds__(kPtThreads, 1) prefix_tc_kernel(const PrefixTc
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (ok) {
             tc_fence_after();
-            float *slot = p.slots + ((static_cast<int64_t>(h) * p.row_blocks + (r >> 3)) * p.splits + split) * (8 * 128 + 16);
-            float la, lb;
-            f2_unpack(l2, la, lb);
+            auto slot_of = [&](int row) {
+                return p.slots + ((static_cast<int64_t>(h) * p.row_blocks + (row >> 3)) * p.splits + split) * (8 * 128 + 16);
+            };
             if (r < p.rows) {
-                slot[8 * 128 + (r & 7)] = m_ref - kLift;
-                slot[8 * 128 + 8 + (r & 7)] = la + lb;
+                float la, lb;
+                f2_unpack(l2, la, lb);
+                slot_of(r)[8 * 128 + (r & 7)] = m_ref - kLift;
+                slot_of(r)[8 * 128 + 8 + (r & 7)] = la + lb;
             }
+            // O rows go through this warp's 16 KB of the K (tile 0) or V (tile 1) stages, 16-byte chunk c
+            // of row i at c ^ i, and out as whole rows.  (Tile 0's last P V completes after every
+            // product with K; after tile 1's nothing reads the stages any more.)
+            const uint32_t buf = sbase + (t == 0 ? kPtK : kPtV) + (warp & 3) * 16384;
 #pragma unroll 1
             for (int c = 0; c < 4; c++) {
                 uint32_t o[32];
                 tmem_ld32_async(oo + 32 * c, o);
                 tmem_wait(o);
-                if (r < p.rows) {
-                    float4 *dst = reinterpret_cast<float4 *>(slot + (r & 7) * 128 + 32 * c);
+                // d = 8 g + (0 .. 7) sits in columns 0, 2, 4, 6, 1, 3, 5, 7 of its 8
 #pragma unroll
-                    for (int g = 0; g < 4; g++) {   // d = 8 g + (0 .. 7) sits in columns 0, 2, 4, 6, 1, 3, 5, 7
-                        dst[2 * g] = make_float4(__uint_as_float(o[8 * g]), __uint_as_float(o[8 * g + 2]),
-                                                 __uint_as_float(o[8 * g + 4]), __uint_as_float(o[8 * g + 6]));
-                        dst[2 * g + 1] = make_float4(__uint_as_float(o[8 * g + 1]), __uint_as_float(o[8 * g + 3]),
-                                                     __uint_as_float(o[8 * g + 5]), __uint_as_float(o[8 * g + 7]));
-                    }
+                for (int g = 0; g < 8; g++) {
+                    const int n = 8 * (g >> 1) + (g & 1);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                                 ::"r"(buf + lane * 512 + (((8 * c + g) ^ lane) << 4)), "r"(o[n]), "r"(o[n + 2]),
+                                 "r"(o[n + 4]), "r"(o[n + 6]) : "memory");
                 }
+            }
+            __syncwarp();
+            const int rw = row0 + 32 * warp;   // this warp's first row
+#pragma unroll 1
+            for (int i = 0; i < 32 && rw + i < p.rows; i += 8) {
+                uint4 u[8];
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    u[k] = lds128(buf + (i + k) * 512 + ((lane ^ (i + k)) << 4));
+                float *dst = slot_of(rw + i) + 4 * lane;
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    if (rw + i + k < p.rows)
+                        *reinterpret_cast<uint4 *>(dst + 128 * k) = u[k];
             }
         }
         tc_fence_before();
