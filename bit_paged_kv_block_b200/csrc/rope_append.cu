@@ -63,8 +63,7 @@ struct RopeParams {
     int32_t interleaved;
     int32_t strided;
     int32_t kv_ctas;           // CTAs [0, kv_ctas) quantize, the others rotate q rows
-    int32_t q_slices;          // a q item is one token's heads [slice * slice_heads, + slice_heads)
-    int32_t slice_heads;
+    int32_t q_slices;          // q items of a token: runs of 4 KB of its heads
     int64_t q_stride;          // bf16 elements between tokens of q
     const uint16_t *q;
     uint16_t *q_out;
@@ -103,84 +102,194 @@ __device__ __forceinline__ uint32_t rotate_word(uint32_t own, uint32_t other, ui
     return bf16x2_as_u32(lo, hi);
 }
 
-// Halves layout: 8 elements `own` of a head vector and the 8 of their partners; cos / sin at the
-// chunk's 8 pairs, the sine's sign flipped for the first half.
-__device__ __forceinline__ uint4 rotate_halves(uint4 own, uint4 other, const float *cos, const float *sin, bool first,
-                                               uint64_t neg0)
-{
-    const float4 c0 = __ldg(reinterpret_cast<const float4 *>(cos)), c1 = __ldg(reinterpret_cast<const float4 *>(cos) + 1);
-    const float4 s0 = __ldg(reinterpret_cast<const float4 *>(sin)), s1 = __ldg(reinterpret_cast<const float4 *>(sin) + 1);
-    const uint64_t flip = first ? 0x8000000080000000ull : 0ull;
-    return make_uint4(rotate_word(own.x, other.x, f2_pack(c0.x, c0.y), f2_pack(s0.x, s0.y) ^ flip, neg0),
-                      rotate_word(own.y, other.y, f2_pack(c0.z, c0.w), f2_pack(s0.z, s0.w) ^ flip, neg0),
-                      rotate_word(own.z, other.z, f2_pack(c1.x, c1.y), f2_pack(s1.x, s1.y) ^ flip, neg0),
-                      rotate_word(own.w, other.w, f2_pack(c1.z, c1.w), f2_pack(s1.z, s1.w) ^ flip, neg0));
-}
+// The cosines and sines of a 16-byte chunk of a head vector, as the pairs its words take, the sines
+// with the sign of the second term: halves layout, 8 pairs' values (negated sines for the first half);
+// interleaved, 4 pairs' values, each for both elements.
+struct ChunkAngles {
+    uint64_t c[4], s[4];
+
+    __device__ __forceinline__ void set_halves(float4 c0, float4 c1, float4 s0, float4 s1, bool first)
+    {
+        const uint64_t flip = first ? 0x8000000080000000ull : 0ull;
+        c[0] = f2_pack(c0.x, c0.y), c[1] = f2_pack(c0.z, c0.w), c[2] = f2_pack(c1.x, c1.y), c[3] = f2_pack(c1.z, c1.w);
+        s[0] = f2_pack(s0.x, s0.y) ^ flip, s[1] = f2_pack(s0.z, s0.w) ^ flip;
+        s[2] = f2_pack(s1.x, s1.y) ^ flip, s[3] = f2_pack(s1.z, s1.w) ^ flip;
+    }
+    __device__ __forceinline__ void set_pairs(float4 a, float4 b)
+    {
+        c[0] = f2_pack(a.x, a.x), c[1] = f2_pack(a.y, a.y), c[2] = f2_pack(a.z, a.z), c[3] = f2_pack(a.w, a.w);
+        s[0] = f2_pack(-b.x, b.x), s[1] = f2_pack(-b.y, b.y), s[2] = f2_pack(-b.z, b.z), s[3] = f2_pack(-b.w, b.w);
+    }
+    // the chunk `own` with its partners `other` (halves: the other half's chunk; pairs: own, swapped)
+    __device__ __forceinline__ uint4 rotate(uint4 own, uint4 other, uint64_t neg0) const
+    {
+        return make_uint4(rotate_word(own.x, other.x, c[0], s[0], neg0), rotate_word(own.y, other.y, c[1], s[1], neg0),
+                          rotate_word(own.z, other.z, c[2], s[2], neg0), rotate_word(own.w, other.w, c[3], s[3], neg0));
+    }
+};
 
 __device__ __forceinline__ uint32_t swap_halves(uint32_t w) { return __byte_perm(w, 0, 0x1032); }
-
-// Interleaved layout: 8 elements, their 4 pairs' cos / sin.
-__device__ __forceinline__ uint4 rotate_pairs(uint4 own, const float *cos, const float *sin, uint64_t neg0)
+__device__ __forceinline__ uint4 swap_pairs(uint4 u)
 {
-    const float4 c = __ldg(reinterpret_cast<const float4 *>(cos)), s = __ldg(reinterpret_cast<const float4 *>(sin));
-    return make_uint4(rotate_word(own.x, swap_halves(own.x), f2_pack(c.x, c.x), f2_pack(-s.x, s.x), neg0),
-                      rotate_word(own.y, swap_halves(own.y), f2_pack(c.y, c.y), f2_pack(-s.y, s.y), neg0),
-                      rotate_word(own.z, swap_halves(own.z), f2_pack(c.z, c.z), f2_pack(-s.z, s.z), neg0),
-                      rotate_word(own.w, swap_halves(own.w), f2_pack(c.w, c.w), f2_pack(-s.w, s.w), neg0));
+    return make_uint4(swap_halves(u.x), swap_halves(u.y), swap_halves(u.z), swap_halves(u.w));
 }
 
-// The q rows: a warp takes one token's heads (or a slice of them), each lane one 16-byte chunk of a
-// head and the same chunk of every 32 / (D / 8)-th head after it.  The partner's chunk comes from
-// its lane by shuffles.
-template <int kD>
-__device__ __forceinline__ void rotate_queries(const RopeParams &p)
-{
-    constexpr int kChunks = kD / 8;                // 16-byte chunks of a head
-    constexpr int kHeads = 32 / kChunks;           // heads a warp holds at once
-    const int lane = threadIdx.x & 31;
-    const int chunk = lane % kChunks, sub = lane / kChunks;
-    const int hc = p.rotary / 16;                  // chunks of half the rotary part
-    const bool turned = chunk < 2 * hc, first = chunk < hc;
-    const int partner = (lane - chunk) + (first ? chunk + hc : chunk - hc);
-    const uint64_t neg0 = f2_pack(p.neg_zero, p.neg_zero);
-    const int64_t items = p.num_tokens * p.q_slices;
-    const int64_t step = static_cast<int64_t>(gridDim.x - p.kv_ctas) * kRqWarps;
-    for (int64_t it = static_cast<int64_t>(blockIdx.x - p.kv_ctas) * kRqWarps + (threadIdx.x >> 5); it < items; it += step) {
-        const int64_t tok = it / p.q_slices;
-        const int h0 = static_cast<int>(it - tok * p.q_slices) * p.slice_heads, h1 = min(p.hq, h0 + p.slice_heads);
-        const int64_t pos = p.positions[tok];
-        if (token_slot(p, p.slots[tok], pos, lane == 0 && h0 == 0) < 0)
-            continue;
-        const float *row = p.table + pos * p.rotary;
-        const float *cos = row + (p.interleaved ? 4 * chunk : 8 * (first ? chunk : chunk - hc));
-        const float *sin = cos + p.rotary / 2;
-        const uint16_t *src = p.q + tok * p.q_stride + 8 * chunk;
-        uint16_t *dst = p.q_out + tok * p.hq * kD + 8 * chunk;
-#pragma unroll 4
-        for (int h = h0 + sub; h - sub < h1; h += kHeads) {
-            const bool in = h < h1;
-            uint4 x = in ? *reinterpret_cast<const uint4 *>(src + h * kD) : make_uint4(0u, 0u, 0u, 0u);
-            if (p.interleaved) {
-                if (turned)
-                    x = rotate_pairs(x, cos, sin, neg0);
-            } else {
-                uint4 y;
-                y.x = __shfl_sync(0xFFFFFFFFu, x.x, partner);
-                y.y = __shfl_sync(0xFFFFFFFFu, x.y, partner);
-                y.z = __shfl_sync(0xFFFFFFFFu, x.z, partner);
-                y.w = __shfl_sync(0xFFFFFFFFu, x.w, partner);
-                if (turned)
-                    x = rotate_halves(x, y, cos, sin, first, neg0);
-            }
-            if (in)
-                *reinterpret_cast<uint4 *>(dst + h * kD) = x;
+// The 8 cosines and sines of chunk pair j, from a table row.
+struct RawAngles {
+    float4 c0, c1, s0, s1;
+    __device__ __forceinline__ void load(const float *row, int rotary, int j)
+    {
+        const float4 *c = reinterpret_cast<const float4 *>(row + 8 * j), *s = reinterpret_cast<const float4 *>(row + rotary / 2 + 8 * j);
+        c0 = __ldg(c), c1 = __ldg(c + 1), s0 = __ldg(s), s1 = __ldg(s + 1);
+    }
+};
+
+// One pair of 16-byte chunks of a rotary part, in shared memory: chunks a and b (halves: j and
+// j + R/16; interleaved: 2 j and 2 j + 1), in place.
+struct PairAngles {
+    ChunkAngles a, b;
+    __device__ __forceinline__ void set(const RawAngles &r, int interleaved)
+    {
+        if (interleaved) {
+            a.set_pairs(r.c0, r.s0);
+            b.set_pairs(r.c1, r.s1);
+        } else {
+            a.set_halves(r.c0, r.c1, r.s0, r.s1, true);
+            b.set_halves(r.c0, r.c1, r.s0, r.s1, false);
         }
     }
+    __device__ __forceinline__ void rotate(uint32_t at_a, uint32_t at_b, int interleaved, uint64_t neg0) const
+    {
+        const uint4 x = lds128(at_a), y = lds128(at_b);
+        sts128(at_a, a.rotate(x, interleaved ? swap_pairs(x) : y, neg0));
+        sts128(at_b, b.rotate(y, interleaved ? swap_pairs(y) : x, neg0));
+    }
+};
+
+__device__ __forceinline__ void bulk_s2g(void *dst, uint32_t src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
+                 "cp.async.bulk.commit_group;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 
-// The k and v rows: tiles of 32 rows of 64 elements, K and V tiles in turn, through a warp's ring of
-// tensor copies; lane = row.  (The quantizer's own kernel gives half its lanes to K and half to V;
-// here a tile is one of them, so that the rotary step never runs with half the lanes idle.)
+// The q rows: an item is up to 4 KB of one token's heads.  A warp copies items into its ring two ahead,
+// rotates them where they are and copies them out, all in bulk: the copies in flight, 64 KB per SM at
+// two such CTAs, are what keeps the memory busy (loads into registers reached half of it).  A lane
+// takes one chunk pair j of every (32 / pairs)-th head, so its angles are loaded once per item.
+template <int kD>
+__device__ __forceinline__ void rotate_queries(const RopeParams &p, uint8_t *smem)
+{
+    constexpr int kStageBytes = 4096, kItemHeads = kStageBytes / (2 * kD);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t ring = smem_u32(smem) + warp * kRqStages * kStageBytes;
+    const uint32_t bar0 = smem_u32(smem + kRqWarps * kRqStages * kStageBytes) + warp * kRqStages * 8;
+    if (lane == 0)
+        for (int i = 0; i < kRqStages; i++)
+            mbar_init(bar0 + 8 * i, 1);
+    mbar_init_fence();
+    __syncwarp();
+    const int pairs = p.rotary / 16, per = 32 / pairs;   // chunk pairs of a head, heads a pass takes
+    const int j = lane % pairs, sub = lane / pairs;
+    const int ca = p.interleaved ? 2 * j : j, cb = p.interleaved ? 2 * j + 1 : j + pairs;
+    const uint64_t neg0 = f2_pack(p.neg_zero, p.neg_zero);
+    const int64_t items = p.num_tokens * p.q_slices, step = static_cast<int64_t>(gridDim.x - p.kv_ctas) * kRqWarps;
+    const int64_t it0 = static_cast<int64_t>(blockIdx.x - p.kv_ctas) * kRqWarps + warp;
+    const int n = it0 < items ? static_cast<int>((items - it0 + step - 1) / step) : 0;
+    // an item of this warp: token, first head and, for a live token, position (else -1); items are
+    // looked at in order, a step apart
+    struct Item {
+        int tok, h0;
+        int pos;
+    };
+    int look_i = 0, look_tok = static_cast<int>(it0 / p.q_slices), look_slice = static_cast<int>(it0 % p.q_slices);
+    const int step_tok = static_cast<int>(step / p.q_slices), step_slice = static_cast<int>(step % p.q_slices);
+    auto look = [&]() -> Item {
+        Item x = {look_tok, look_slice * kItemHeads, -1};
+        if (look_i < n) {
+            const int64_t pos = p.positions[x.tok];
+            if (token_slot(p, p.slots[x.tok], pos, lane == 0 && x.h0 == 0) >= 0)
+                x.pos = static_cast<int>(pos);
+        }
+        look_i++;
+        look_tok += step_tok;
+        look_slice += step_slice;
+        if (look_slice >= p.q_slices) {
+            look_slice -= p.q_slices;
+            look_tok++;
+        }
+        return x;
+    };
+    auto heads_of = [&](const Item &x) { return min(kItemHeads, p.hq - x.h0); };
+    RawAngles raw;
+    auto angles = [&](const Item &x) {
+        if (x.pos >= 0)
+            raw.load(p.table + static_cast<int64_t>(x.pos) * p.rotary, p.rotary, j);
+    };
+    uint32_t phases = 0, queued = 0;   // per stage: the parity of its next completion (a skipped item
+                                       // uses no stage); whether a copy is on its way
+    auto issue = [&](int i, const Item &x) {
+        if (x.pos < 0)
+            return;
+        queued |= 1u << (i % kRqStages);
+        if (lane == 0) {
+            const uint32_t bytes = static_cast<uint32_t>(heads_of(x)) * kD * 2, bar = bar0 + 8 * (i % kRqStages);
+            mbar_arrive_expect_tx(bar, bytes);
+            bulk_g2s(ring + (i % kRqStages) * kStageBytes, p.q + x.tok * p.q_stride + x.h0 * kD, bytes, bar);
+        }
+    };
+    Item cur = look(), next = look(), after = look();
+    issue(0, cur);
+    issue(1, next);
+    angles(cur);
+    for (int i = 0; i < n; i++) {
+        // the stage of item i + 2 is that of item i - 1, whose copy out has to have read it
+        if (lane == 0)
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        issue(i + 2, after);
+        const Item far = look();
+        PairAngles ang;
+        ang.set(raw, p.interleaved);
+        angles(next);
+        if (cur.pos >= 0) {
+            const int stg = i % kRqStages;
+            const bool ok = mbar_wait_bounded(bar0 + 8 * stg, (phases >> stg) & 1u, kRqWaitLimitNs);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                if (lane == 0)
+                    set_status(p.status, SAW_DEV_WAIT_TIMEOUT);
+                break;
+            }
+            phases ^= 1u << stg;
+            queued &= ~(1u << stg);
+            const uint32_t stage = ring + stg * kStageBytes;
+            if (sub < per) {
+#pragma unroll 2
+                for (int h = sub; h < heads_of(cur); h += per)
+                    ang.rotate(stage + h * (2 * kD) + 16 * ca, stage + h * (2 * kD) + 16 * cb, p.interleaved, neg0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0)
+                bulk_s2g(p.q_out + (static_cast<int64_t>(cur.tok) * p.hq + cur.h0) * kD, stage,
+                         static_cast<uint32_t>(heads_of(cur)) * kD * 2);
+        }
+        cur = next;
+        next = after;
+        after = far;
+    }
+    // copies in (after a wait that gave up) and out are over before the shared memory is released
+    for (int k = 0; k < kRqStages; k++)
+        if ((queued >> k) & 1u)
+            mbar_wait_bounded(bar0 + 8 * k, (phases >> k) & 1u, kRqWaitLimitNs / 10);
+    if (lane == 0)
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// The k and v rows: tiles of 32 rows of 64 elements through a warp's ring of tensor copies; lane = row.
+// (The quantizer's own kernel gives half its lanes to K and half to V; here a tile is one of them, so
+// that the rotary step never runs with half the lanes idle.)  A warp takes K and V tiles in turn: K
+// tiles cost half as much again.  A tile's slots and positions are loaded two tiles ahead and the
+// table rows that its K vectors need are prefetched one tile ahead: read where they are used, they
+// cost as much as the quantizer (192 us instead of 120 for 65,536 tokens x 8 kv heads).
 template <bool kRotate, int kD>
 __device__ __forceinline__ void quantize_tiles(const CUtensorMap &tk, const CUtensorMap &tv, const RopeParams &p,
                                                uint8_t *smem)
@@ -203,17 +312,21 @@ __device__ __forceinline__ void quantize_tiles(const CUtensorMap &tk, const CUte
     mbar_init_fence();
     __syncwarp();
 
+    // this warp's i-th tile: item t = wg + i W is tile t / 2 of K or V, the two halves of a tile going
+    // to neighbouring warps that swap roles every turn (W is even)
+    auto tile_of = [&](int i) { return (wg + i * W) >> 1; };
+    auto half_of = [&](int i) { return static_cast<int>((wg + i) & 1u); };
+
     int issued = 0;
-    // queue tile wg + issued W: two boxes of 16 rows (of one token's rows, or of whole tokens)
+    // queue the next tile: two boxes of 16 rows (of one token's rows, or of whole tokens)
     auto issue = [&]() {
         if (issued < n && lane == 0) {
-            const uint32_t tile = wg + issued * W;
             const uint32_t dst = ring + (issued % kRqStages) * kStageBytes, bar = bar0 + 8 * (issued % kRqStages);
-            const CUtensorMap *map = (tile & 1) ? &tv : &tk;
+            const CUtensorMap *map = half_of(issued) ? &tv : &tk;
             mbar_arrive_expect_tx(bar, kStageBytes);
 #pragma unroll
             for (int b = 0; b < 2; b++) {
-                const uint32_t row = (tile >> 1) * 32 + 16 * b;
+                const uint32_t row = tile_of(issued) * 32 + 16 * b;
                 if (p.strided) {
                     const uint32_t per = static_cast<uint32_t>(p.hkv) * kTpv;   // rows of a token
                     const uint32_t tok = row / per;
@@ -232,16 +345,38 @@ __device__ __forceinline__ void quantize_tiles(const CUtensorMap &tk, const CUte
     const uint32_t num_vecs = static_cast<uint32_t>(p.num_vecs), hkv = static_cast<uint32_t>(p.hkv);
     const int hc = p.rotary / 16;
     const uint64_t neg0 = f2_pack(p.neg_zero, p.neg_zero);
+    // slot and position of this lane's vector in the warp's i-th tile (-1: no such vector)
+    auto vec_of = [&](int i) { return tile_of(i) * kTileVecs + vt; };
+    auto look = [&](int i, int64_t &slot, int64_t &pos) {
+        const uint32_t vec = vec_of(i);
+        const bool in = i < n && vec < num_vecs;
+        const uint32_t tok = in ? vec / hkv : 0;
+        slot = in ? p.slots[tok] : -1;
+        pos = in ? p.positions[tok] : 0;
+    };
+    // the 128-byte lines of a K vector's table row, shared out among the lanes of its token
+    const int lines = (4 * p.rotary + 127) / 128, span = min(lines, min(32, static_cast<int>(hkv) * kTpv));
+    auto prefetch_row = [&](int i, int64_t slot, int64_t pos) {
+        if (half_of(i) == 0 && slot >= 0 && pos >= 0 && pos < p.num_positions)
+            for (int b = lane % span; b < lines; b += span)
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(p.table + pos * p.rotary + 32 * b));
+    };
+    int64_t slot_a, pos_a, slot_b, pos_b;   // of tiles i and i + 1
+    look(0, slot_a, pos_a);
+    look(1, slot_b, pos_b);
+    prefetch_row(0, slot_a, pos_a);
     int i = 0;
     for (; i < n; i++) {
         issue();
-        const uint32_t tile = wg + i * W;
-        const int half = tile & 1;
-        const uint32_t vec_raw = (tile >> 1) * kTileVecs + vt;
-        const uint32_t vec = min(vec_raw, num_vecs - 1);
-        const uint32_t tok = vec / hkv, h = vec - tok * hkv;
-        const int64_t pos = p.positions[tok];
-        const int64_t slot = vec_raw < num_vecs ? token_slot(p, p.slots[tok], pos, part == 0 && half == 0) : -1;
+        const int half = half_of(i);
+        const uint32_t vec = vec_of(i);
+        const uint32_t h = vec % hkv;
+        const int64_t pos = pos_a, slot = token_slot(p, slot_a, pos, part == 0 && half == 0);
+        slot_a = slot_b;
+        pos_a = pos_b;
+        if (i + 1 < n)
+            prefetch_row(i + 1, slot_a, pos_a);
+        look(i + 2, slot_b, pos_b);
         const int stg = i % kRqStages;
         const bool ok = mbar_wait_bounded(bar0 + 8 * stg, (i / kRqStages) & 1, kRqWaitLimitNs);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -252,26 +387,31 @@ __device__ __forceinline__ void quantize_tiles(const CUtensorMap &tk, const CUte
         // 16-byte chunk c of row r sits at chunk c ^ (r & 7) under the 128-byte swizzle
         const uint32_t stage = ring + stg * kStageBytes;
         auto chunk_at = [&](int r, int c) { return lds128(stage + r * 128 + ((c ^ (r & 7)) << 4)); };
-        // a skipped token's position may be anything: rotate it by the table's first row
-        const float *cos = p.table + (slot >= 0 ? pos : 0) * p.rotary, *sin = cos + p.rotary / 2;
-        auto load = [&](int c) -> uint4 {
-            const uint4 own = chunk_at(lane, c);
-            const int vc = 8 * part + c;   // chunk of the head vector
-            if (half != 0 || vc >= 2 * hc)
-                return own;
-            if (p.interleaved)
-                return rotate_pairs(own, cos + 4 * vc, sin + 4 * vc, neg0);
-            const bool first = vc < hc;
-            const int pc = first ? vc + hc : vc - hc;
-            const uint4 other = chunk_at(vt * kTpv + (pc >> 3), pc & 7);
-            const int at = 8 * (first ? vc : pc);
-            return rotate_halves(own, other, cos + at, sin + at, first, neg0);
-        };
+        if (half == 0) {
+            // The rotary step, in place: pair j of a vector's chunks (halves: chunks j and j + hc; interleaved:
+            // 2 j and 2 j + 1) takes the same 8 cosines and sines in either layout; the vector's lanes share
+            // the pairs.  Rolled: unrolled over the row's chunks beside the quantizer, the loop no longer
+            // fitted the instruction cache.  (A skipped token is rotated by the table's first row.)
+            const float *cos = p.table + (slot >= 0 ? pos : 0) * p.rotary;
+#pragma unroll 1
+            for (int j = part; j < hc; j += kTpv) {
+                RawAngles raw;
+                raw.load(cos, p.rotary, j);
+                PairAngles ang;
+                ang.set(raw, p.interleaved);
+                const int ca = p.interleaved ? 2 * j : j, cb = p.interleaved ? 2 * j + 1 : j + hc;
+                const int ra = vt * kTpv + (ca >> 3), rb = vt * kTpv + (cb >> 3);
+                ang.rotate(stage + ra * 128 + (((ca & 7) ^ (ra & 7)) << 4), stage + rb * 128 + (((cb & 7) ^ (rb & 7)) << 4),
+                           p.interleaved, neg0);
+            }
+            __syncwarp();
+        }
         uint64_t X[kN];
 #pragma unroll
         for (int c = 0; c < 4; c++)
-            pairs_from_chunk(load(c), load(c + 4), X + 8 * c);
-        __syncwarp();   // every lane has read the stage
+            pairs_from_chunk(chunk_at(lane, c), chunk_at(lane, c + 4), X + 8 * c);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the stage was written here
+        __syncwarp();   // every lane has read it
         if constexpr (kRotate) {
             fwht_stages<kN>(X);
             if constexpr (kD == 64) {
@@ -311,12 +451,11 @@ __global__ void __launch_bounds__(kRqThreads, 4)
 {
     extern __shared__ uint8_t smem_raw[];
     pdl_launch_dependents();
-    if (static_cast<int>(blockIdx.x) >= p.kv_ctas) {
-        rotate_queries<kD>(p);
-        return;
-    }
-    quantize_tiles<kRotate, kD>(
-        tk, tv, p, reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023)));
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    if (static_cast<int>(blockIdx.x) >= p.kv_ctas)
+        rotate_queries<kD>(p, smem);
+    else
+        quantize_tiles<kRotate, kD>(tk, tv, p, smem);
 }
 
 // Tensor map of k or v: [rows][128 B] for contiguous tokens (stride 0), else [tokens][rows of a
@@ -354,11 +493,13 @@ cudaError_t launch(const RopeAppendArgs &a, RopeParams &p, const CUtensorMap &tk
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
     if (e != cudaSuccess)
         return e;
-    // 4 CTAs per SM in all; the q rows get half of them where there is enough work
+    // 4 CTAs per SM in all, shared out by what a 64-element row costs: a k or v row about twice a
+    // q row (each role gets what the other does not need)
     const int64_t q_items = p.num_tokens * p.q_slices;
     const int64_t kv_need = (p.num_tiles + kRqWarps - 1) / kRqWarps, q_need = p.hq > 0 ? (q_items + kRqWarps - 1) / kRqWarps : 0;
     const int64_t room = 4 * static_cast<int64_t>(sms);
-    p.kv_ctas = static_cast<int32_t>(std::min(kv_need, p.hq > 0 ? room / 2 : room));
+    const int64_t kv_share = std::max<int64_t>(1, room * 4 * p.hkv / (4 * p.hkv + p.hq));
+    p.kv_ctas = static_cast<int32_t>(std::min(kv_need, std::max(kv_share, room - q_need)));
     const int64_t q_ctas = std::min(q_need, room - p.kv_ctas);
     kernel<<<static_cast<unsigned>(p.kv_ctas + q_ctas), kRqThreads, kSmem, stream>>>(tk, tv, p);
     return cudaGetLastError();
@@ -415,10 +556,8 @@ cudaError_t launch_rope_append(const RopeAppendArgs &a, cudaStream_t stream)
     p.mass = a.mass;
     p.status = kv.status;
     p.neg_zero = -0.0f;
-    // few tokens: a warp takes 2 passes over the heads it holds, so that the call spreads over the SMs
-    const int heads = 32 / (kv.head_dim / 8);
-    p.slice_heads = kv.num_tokens >= 4096 ? std::max(1, a.num_q_heads) : 2 * heads;
-    p.q_slices = a.num_q_heads > 0 ? (a.num_q_heads + p.slice_heads - 1) / p.slice_heads : 1;
+    const int item_heads = 4096 / (2 * kv.head_dim);
+    p.q_slices = a.num_q_heads > 0 ? (a.num_q_heads + item_heads - 1) / item_heads : 1;
     switch (kv.head_dim) {
     case 64:
         return kv.rotate ? launch<true, 64>(a, p, tk, tv, stream) : launch<false, 64>(a, p, tk, tv, stream);
