@@ -147,7 +147,9 @@ struct SeqTables {
 constexpr int kModeDecode = 0;
 constexpr int kModePrefill = 1;
 constexpr int kModePrefix = 2;
-constexpr int kMinSlice = 4;   // Plan::init's min_slice of a shared-prefix decode
+// Plan::init's min_slice where the pieces are joined by row_merge.cuh: joining a row's pieces costs about
+// as much per piece as attending over a page, so small launches stop at 4 pages a warp
+constexpr int kRowMinSlice = 4;
 
 // Query tokens of sequence s (decode: 1) and its first query row; the decode instantiation has
 // none of the per-row arithmetic.
@@ -736,7 +738,7 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
         return;
     }
     Plan plan;
-    plan.init(tb, S, p.total_warps, kMode == kModePrefix ? kMinSlice : 1);
+    plan.init(tb, S, p.total_warps, Fmt::kRowPieces ? kRowMinSlice : 1);
     const int64_t u = static_cast<int64_t>(blockIdx.x) * Fmt::kWarps + warp;
     int64_t F0, F1;
     if (p.win_part == 1) {
@@ -975,7 +977,11 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
                 pdl_wait();   // the window part's rows and lse
             Fmt::finalize(p, sg, lane, st.o, st.m, st.l);
         } else {
-            store_partial(p.partials + (tb.spre[cs] + cj + u) * slot_floats<Fmt::kTiles>(), lane, st);
+            float *slot = p.partials + (tb.spre[cs] + cj + u) * slot_floats<Fmt::kTiles>();
+            if constexpr (Fmt::kRowPieces)
+                store_partial_rows(slot, lane, st);
+            else
+                store_partial(slot, lane, st);
         }
         pos = F0 + m_end;
         cs = ns;

@@ -493,10 +493,11 @@ struct Int4Format {
     static_assert(kD == 64 || kD == 128 || kD == 256, "head dimension");
     static constexpr int kDim = kD;
     static constexpr bool kLogits = kRole == kRoleMass;
+    static constexpr bool kRowPieces = kRole == kRoleMass || kRole == kRolePrefix;
     static constexpr int kTiles = kD / 16;
     static constexpr int kWarps = 4;
     static constexpr int kStages = kD == 256 ? 2 : 4;
-    static constexpr int kMinBlocks = kD == 64 ? 5 : kD == 128 ? 4 : 3;
+    static constexpr int kMinBlocks = kD == 64 ? 5 : kD == 128 ? 4 : kRole == kRoleMass ? 2 : 3;
     static constexpr int kRowsPerPage = 32;
     static constexpr int kCodeBytes = code_bytes(kD);
     static constexpr int kRingBytes = kWarps * kStages * (kCodeBytes + kScaleBytes);

@@ -54,7 +54,7 @@ __device__ __forceinline__ uint32_t bf16_chunk(int sel, int tok, int d0)
 // denominator (a separate instantiation, so the plain decode carries none of it).
 template <bool kLse>
 struct Bf16FormatT {
-    static constexpr bool kLogits = false;
+    static constexpr bool kLogits = false, kRowPieces = false;
     static constexpr int kDim = kHeadDim;
     static constexpr int kTiles = kHeadDim / 16;
     static constexpr int kWarps = 4;

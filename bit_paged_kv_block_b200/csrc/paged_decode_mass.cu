@@ -17,7 +17,7 @@
 // tensor cores as fp16 high and low parts (the codes are exact there).
 #include <algorithm>
 
-#include "int4_format.cuh"
+#include "row_merge.cuh"
 
 namespace saw {
 namespace {
@@ -25,7 +25,6 @@ namespace {
 struct MassParams {
     DecodeParams d;
     float *mass;             // fp32 [num_pages][Hkv][16]
-    int32_t blocks_per_kv;   // row blocks of a kv head: ceil(G / 8)
 };
 
 constexpr int kMassThreads = 256;
@@ -35,9 +34,12 @@ inline size_t mass_smem_bytes(int32_t num_seqs)
     return 16 * (kMassThreads / 32) + seq_table_bytes(num_seqs);
 }
 
-// One half warp per (sequence, kv head, page), lane = token.  Tokens of one page and kv head are
-// owned by one lane, which sums its heads in a fixed order; the add is a reduction without return,
-// so it is exact-order unless two sequences of the call share a page.
+// The (sequence, kv head, page) triples lie end to end, and every warp takes one run of them: it looks
+// its place up once, keeps the rows' lse of the current kv head in registers, and adds up two pages at
+// a time, half a warp each, lane = token.  A token of one sequence and kv head is owned by one lane, which
+// sums its heads in a fixed order; the add is a reduction without return, so the result repeats
+// unless two sequences of the call share a page.  kBlocks: row blocks of a kv head, ceil(G / 8).
+template <int kBlocks>
 __global__ void __launch_bounds__(kMassThreads) mass_accumulate_kernel(const MassParams mp)
 {
     const DecodeParams &p = mp.d;
@@ -48,27 +50,68 @@ __global__ void __launch_bounds__(kMassThreads) mass_accumulate_kernel(const Mas
     scan_sequences<kModeDecode>(p, tb, flags, false);
     Plan plan;
     plan.init(tb, p.num_seqs, p.total_warps);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tok = lane & 15, sub = lane >> 4;
+    const int64_t units = plan.P / kBlocks, warps = static_cast<int64_t>(gridDim.x) * (kMassThreads / 32);
+    const int64_t per = (units + warps - 1) / warps;
+    int64_t u = (static_cast<int64_t>(blockIdx.x) * (kMassThreads / 32) + warp) * per;
+    const int64_t u1 = min(units, u + per);
     pdl_wait();   // logits and lse
-    const int nb = mp.blocks_per_kv, tok = threadIdx.x & 15;
-    const int64_t units = plan.P / nb, step = static_cast<int64_t>(gridDim.x) * (kMassThreads / 16);
-    for (int64_t u = (static_cast<int64_t>(blockIdx.x) * kMassThreads + threadIdx.x) / 16; u < units; u += step) {
-        const int s = plan.seq_of_flat(u * nb);
-        const int n = tb.npg[s];
-        const int rel = static_cast<int>(u - tb.fpre[s] / nb);
-        const int h = rel / n, i = rel - h * n;
-        const int32_t page = p.block_table[static_cast<int64_t>(s) * p.max_blocks + i];
-        if (page < 0 || page >= p.num_pages || kPageSize * i + tok >= p.seq_lens[s])
-            continue;
-        float sum = 0.0f;
-        for (int b = 0; b < nb; b++) {
-            const int rows = min(kRowsPerBlock, p.group - kRowsPerBlock * b);
-            const float *lg = p.logits + ((tb.fpre[s] + static_cast<int64_t>(h * nb + b) * n + i) * kPageSize + tok) *
-                                             p.qrows;
-            const float *lse = p.lse + static_cast<int64_t>(s) * p.hq + h * p.group + kRowsPerBlock * b;
-            for (int c = 0; c < rows; c++)
-                sum += ex2_approx(lg[c] - lse[c]);
+    if (u >= u1)
+        return;
+    int s = plan.seq_of_flat(u * kBlocks);
+    int h = static_cast<int>((u - tb.fpre[s] / kBlocks) / tb.npg[s]);
+    int i = static_cast<int>(u - tb.fpre[s] / kBlocks) - h * tb.npg[s];
+    while (true) {
+        const int n = tb.npg[s], len = p.seq_lens[s];
+        const int i1 = static_cast<int>(min(static_cast<int64_t>(n), i + (u1 - u)));   // pages [i, i1) of (s, h)
+        float lse[kBlocks][kRowsPerBlock];
+#pragma unroll
+        for (int b = 0; b < kBlocks; b++)
+#pragma unroll
+            for (int c = 0; c < kRowsPerBlock; c++) {
+                const int g = kRowsPerBlock * b + c;   // a row past the group: weight 2^(-inf)
+                lse[b][c] = g < p.group ? p.lse[static_cast<int64_t>(s) * p.hq + h * p.group + g] : INFINITY;
+            }
+        const int32_t *table = p.block_table + static_cast<int64_t>(s) * p.max_blocks;
+        const float *lg0 = p.logits + ((tb.fpre[s] + static_cast<int64_t>(h) * kBlocks * n) * kPageSize + tok) * p.qrows;
+#pragma unroll 4
+        for (int k = i + sub; k < i1; k += 2) {
+            const int32_t page = table[k];
+            float sum = 0.0f;
+#pragma unroll
+            for (int b = 0; b < kBlocks; b++) {
+                const float *lg = lg0 + (static_cast<int64_t>(b) * n + k) * (kPageSize * p.qrows);
+                if (p.qrows == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(lg);
+                    sum += (ex2_approx(x.x - lse[b][0]) + ex2_approx(x.y - lse[b][1])) +
+                           (ex2_approx(x.z - lse[b][2]) + ex2_approx(x.w - lse[b][3]));
+                } else if (p.qrows == 8) {
+                    const float4 x = *reinterpret_cast<const float4 *>(lg), y = *reinterpret_cast<const float4 *>(lg + 4);
+                    const int rows = p.group - kRowsPerBlock * b;   // columns past the group were not written
+                    sum += (ex2_approx(x.x - lse[b][0]) + (rows > 1 ? ex2_approx(x.y - lse[b][1]) : 0.0f)) +
+                           ((rows > 2 ? ex2_approx(x.z - lse[b][2]) : 0.0f) + (rows > 3 ? ex2_approx(x.w - lse[b][3]) : 0.0f)) +
+                           ((rows > 4 ? ex2_approx(y.x - lse[b][4]) : 0.0f) + (rows > 5 ? ex2_approx(y.y - lse[b][5]) : 0.0f)) +
+                           ((rows > 6 ? ex2_approx(y.z - lse[b][6]) : 0.0f) + (rows > 7 ? ex2_approx(y.w - lse[b][7]) : 0.0f));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kRowsPerBlock; c++)
+                        if (c < p.qrows)
+                            sum += ex2_approx(lg[c] - lse[b][c]);
+                }
+            }
+            if (page >= 0 && page < p.num_pages && kPageSize * k + tok < len)
+                atomicAdd(mp.mass + (static_cast<int64_t>(page) * p.hkv + h) * kPageSize + tok, sum);
         }
-        atomicAdd(mp.mass + (static_cast<int64_t>(page) * p.hkv + h) * kPageSize + tok, sum);
+        u += i1 - i;
+        if (u >= u1)
+            break;
+        i = 0;
+        if (++h == p.hkv) {
+            h = 0;
+            do
+                s++;
+            while (tb.npg[s] == 0);
+        }
     }
 }
 
@@ -85,10 +128,10 @@ cudaError_t mass_shape(size_t smem, size_t merge_smem, LaunchShape &out)
         reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<true, kD>, kModeDecode>),
         reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<false, kD>, kModeDecode>)};
     static const void *const merge_kernels[kShapeVariants] = {
-        reinterpret_cast<const void *>(paged_decode_merge_kernel<MassFormat<true, kD>, kModeDecode>),
-        reinterpret_cast<const void *>(paged_decode_merge_kernel<MassFormat<false, kD>, kModeDecode>),
-        reinterpret_cast<const void *>(paged_decode_merge_kernel<MassFormat<true, kD>, kModeDecode>),
-        reinterpret_cast<const void *>(paged_decode_merge_kernel<MassFormat<false, kD>, kModeDecode>)};
+        reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModeDecode>),
+        reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModeDecode>),
+        reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModeDecode>),
+        reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModeDecode>)};
     return decode::launch_shape(shapes, decode_kernels, merge_kernels, 32 * MassFormat<true, kD>::kWarps,
                                 smem, merge_smem, out);
 }
@@ -105,7 +148,7 @@ cudaError_t mass_workspace(int32_t hkv, int32_t hq, int32_t num_seqs, int32_t ma
     using Fmt = MassFormat<true, kD>;
     const int32_t qrows = query_rows(hkv, hq, false);
     const cudaError_t e = mass_shape<kD>(decode_smem_bytes<Fmt>(num_seqs, qrows),
-                                         merge_smem_bytes<Fmt::kTiles>(num_seqs), ls);
+                                         row_merge_smem(num_seqs), ls);
     if (e != cudaSuccess)
         return e;
     const int64_t segments = max_segments(hkv, hq, num_seqs, 0, false);
@@ -137,7 +180,6 @@ cudaError_t launch(const DecodeArgs &a, float *mass, cudaStream_t stream, bool p
     p.lse = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + w.lse);
     p.logits = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + w.logits);
     mp.mass = mass;
-    mp.blocks_per_kv = (p.group + kRowsPerBlock - 1) / kRowsPerBlock;
 
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -153,18 +195,19 @@ cudaError_t launch(const DecodeArgs &a, float *mass, cudaStream_t stream, bool p
     if (e != cudaSuccess)
         return e;
 
-    cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(p.max_segments, 8 * ls.sms))));
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.dynamicSmemBytes = merge_smem_bytes<Fmt::kTiles>(a.num_seqs);
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(p.max_segments, 16 * ls.sms)));
+    cfg.blockDim = dim3(32 * kRowWarps);
+    cfg.dynamicSmemBytes = row_merge_smem(a.num_seqs);
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, paged_decode_merge_kernel<Fmt, kModeDecode>, p);
+    e = cudaLaunchKernelEx(&cfg, row_merge_kernel<kRotate, kD, kModeDecode>, p, PrefixPieces{nullptr, 0, 0});
     if (e != cudaSuccess)
         return e;
 
     cfg.gridDim = dim3(static_cast<unsigned>(4 * ls.sms));
     cfg.blockDim = dim3(kMassThreads);
     cfg.dynamicSmemBytes = mass_smem_bytes(a.num_seqs);
-    e = cudaLaunchKernelEx(&cfg, mass_accumulate_kernel, mp);
+    e = p.group <= kRowsPerBlock ? cudaLaunchKernelEx(&cfg, mass_accumulate_kernel<1>, mp)
+                                 : cudaLaunchKernelEx(&cfg, mass_accumulate_kernel<2>, mp);
     if (e != cudaSuccess)
         return e;
     return cudaGetLastError();
