@@ -7,10 +7,14 @@
 // other tokens for other heads.  The old pages are only read: they may be shared with other
 // sequences, and go back to the allocator afterwards.
 //
-// Two kernels.  The selection (a CTA per sequence and kv head) finds the need-th largest mass by a
-// radix select over the masses' bits (non-negative floats order as their bits) and writes the kept
-// tokens' indices; the move (a warp per new page and kv head) gathers the rows.  Both are bound by
-// the bytes of the masses and of the kept rows.
+// Two kernels.  The selection (a CTA per sequence and kv head, or a cluster of up to 8 that share its
+// tokens where there are few) holds the masses in shared memory as integer keys (non-negative floats order as their bits) and narrows [lo, hi) around the need-th
+// largest: a histogram of the range in 1024 bins, the bin that holds it, again; at most 4 passes, and
+// since the range starts at the masses' own, the bins are spread over and their counters rarely
+// collide.  Then it writes the kept tokens' indices in order.  The move (a warp per new page and kv
+// head) gathers the rows.  Both are bound by the bytes of the masses and of the kept rows.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "saw_device.cuh"
@@ -19,9 +23,9 @@
 namespace saw {
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelSmemKeys = 49152;   // masses held in shared memory (192 KiB); more are read again
+constexpr int kBins = 1024;
+constexpr uint32_t kFixed = 0xFFFFFFFFu;   // the key of a sink or recent token
 
 struct EvictParams {
     uint8_t *kv_pages;
@@ -42,9 +46,11 @@ struct EvictParams {
     uint32_t *status;
 };
 
-// Inclusive sum over the CTA of (a, b) packed in 64 bits; every thread gets its own prefix and the total.
+// Inclusive sum over the CTA; every thread gets its own prefix and the total.
+template <int kThreads>
 __device__ __forceinline__ uint64_t cta_scan(uint64_t v, uint64_t *warp_sums, uint64_t &total)
 {
+    constexpr int kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t x = v;
 #pragma unroll
@@ -56,138 +62,227 @@ __device__ __forceinline__ uint64_t cta_scan(uint64_t v, uint64_t *warp_sums, ui
     if (lane == 31)
         warp_sums[warp] = x;
     __syncthreads();
-    uint64_t w = lane < kSelWarps ? warp_sums[lane] : 0;
+    uint64_t w = lane < kWarps ? warp_sums[lane] : 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
+    for (int d = 1; d < kWarps; d <<= 1) {
         const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, w, d);
         if (lane >= d)
             w += y;
     }
     const uint64_t before = __shfl_sync(0xFFFFFFFFu, w, max(warp - 1, 0));
-    total = __shfl_sync(0xFFFFFFFFu, w, 31);
+    total = __shfl_sync(0xFFFFFFFFu, w, kWarps - 1);
     __syncthreads();
     return x + (warp > 0 ? before : 0);
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p)
+// A cluster of C CTAs per (sequence, kv head); rank r takes tokens [r chunk, (r + 1) chunk).  Every CTA
+// reads the others' extremes, histograms and counts from their shared memory and draws the same
+// conclusions, so each step costs one cluster barrier.
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel(const EvictParams p)
 {
-    extern __shared__ uint32_t keys[];
-    __shared__ uint32_t hist[256];
-    __shared__ uint64_t warp_sums[kSelWarps];
-    __shared__ uint32_t sh_digit, sh_need;
-    pdl_launch_dependents();
-    const int tid = threadIdx.x;
-    const int s = blockIdx.x / p.hkv, h = blockIdx.x - s * p.hkv;
-    int32_t *kept = p.kept + static_cast<int64_t>(blockIdx.x) * p.keep;
+    extern __shared__ __align__(16) uint32_t keys[];
+    __shared__ __align__(16) uint32_t hist[2][kBins], joint[kBins];   // of this pass and of the one before; the cluster's
+    __shared__ uint64_t warp_sums[kThreads / 32];
+    __shared__ uint32_t sh_lo, sh_hi, sh_bin, sh_need;
+    __shared__ uint64_t sh_count;
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int seg = blockIdx.x / C, s = seg / p.hkv, h = seg - s * p.hkv;
+    int32_t *kept = p.kept + static_cast<int64_t>(seg) * p.keep;
     int L = p.seq_lens[s];
     // a length out of range, or more kept tokens than the new pages hold: left out
     const bool valid = L >= 0 && L <= p.max_blocks * kPageSize && min(L, p.keep) <= p.new_blocks * kPageSize;
     if (!valid) {
-        if (tid == 0 && h == 0)
+        if (tid == 0 && h == 0 && rank == 0)
             set_status(p.status, SAW_DEV_BAD_SEQ_LEN);
         L = 0;
     }
     const int n = min(L, p.keep);
-    if (tid == 0 && h == 0)
+    if (tid == 0 && h == 0 && rank == 0)
         p.new_lens[s] = n;
-    for (int j = n + tid; j < p.keep; j += kSelThreads)
+    for (int j = n + rank * kThreads + tid; j < p.keep; j += C * kThreads)
         kept[j] = -1;
     if (L <= p.keep) {
-        for (int j = tid; j < n; j += kSelThreads)
+        for (int j = rank * kThreads + tid; j < n; j += C * kThreads)
             kept[j] = j;
         return;
     }
-    // the middle tokens [sink, sink + M): keep `need` of them
-    const int M = L - p.sink - p.recent;
-    const uint32_t want = static_cast<uint32_t>(p.keep - p.sink - p.recent);
     const int32_t *table = p.block_table + static_cast<int64_t>(s) * p.max_blocks;
-    const bool in_smem = M <= p.smem_keys;
-    // order-preserving key of middle token i; a NaN or negative mass counts as 0
-    auto read_key = [&](int i) -> uint32_t {
-        const int t = p.sink + i;
-        const int32_t page = table[t / kPageSize];
-        if (page < 0 || page >= p.num_pages) {
+    const int held = p.sink, tail = L - p.recent;
+    const int chunk = ((L + C - 1) / C + kPageSize - 1) / kPageSize * kPageSize;   // whole pages
+    const int t0 = min(L, rank * chunk), t1 = min(L, t0 + chunk);
+    const bool in_smem = chunk <= p.smem_keys;
+    // order-preserving keys of tokens 4 q .. 4 q + 3; a NaN or negative mass counts as 0, a token past
+    // the end is never counted
+    auto read4 = [&](int q) -> uint4 {
+        const int32_t page = table[q / 4];
+        float4 m = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (page >= 0 && page < p.num_pages)
+            m = *reinterpret_cast<const float4 *>(p.mass + (static_cast<int64_t>(page) * p.hkv + h) * kPageSize + 4 * (q & 3));
+        else
             set_status(p.status, SAW_DEV_BAD_PAGE);
-            return 0;
-        }
-        const float m = p.mass[(static_cast<int64_t>(page) * p.hkv + h) * kPageSize + t % kPageSize];
-        return m > 0.0f ? __float_as_uint(m) : 0u;
+        auto key_of = [&](int t, float x) { return t < held || t >= tail ? kFixed : x > 0.0f ? __float_as_uint(x) : 0u; };
+        return make_uint4(key_of(4 * q, m.x), key_of(4 * q + 1, m.y), key_of(4 * q + 2, m.z), key_of(4 * q + 3, m.w));
     };
-    if (in_smem) {
-        for (int i = tid; i < M; i += kSelThreads)
-            keys[i] = read_key(i);
+    const int q0 = t0 / 4, quads = (t1 + 3) / 4;   // t0 is a multiple of 16
+    uint32_t lo = kFixed, hi = 0;
+    if (tid == 0) {
+        sh_lo = kFixed;
+        sh_hi = 0;
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int q = q0 + tid; q < quads; q += kThreads) {
+        const uint4 k = read4(q);
+        if (in_smem)
+            *reinterpret_cast<uint4 *>(keys + 4 * (q - q0)) = k;
+        const uint32_t e[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int c = 0; c < 4; c++)
+            if (e[c] != kFixed) {
+                lo = min(lo, e[c]);
+                hi = max(hi, e[c]);
+            }
+    }
+    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+    if (lane == 0) {
+        atomicMin(&sh_lo, lo);
+        atomicMax(&sh_hi, hi);
+    }
+    cluster.sync();
+    lo = sh_lo;
+    hi = sh_hi;
+    for (int r = 0; r < C; r++) {
+        lo = min(lo, *cluster.map_shared_rank(&sh_lo, r));
+        hi = max(hi, *cluster.map_shared_rank(&sh_hi, r));
+    }
+    // tokens past the end hold kFixed too; every loop below stops at t1
+    auto each4 = [&](int q, auto f) {
+        const uint4 k = in_smem ? *reinterpret_cast<const uint4 *>(keys + 4 * (q - q0)) : read4(q);
+        const uint32_t e[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int c = 0; c < 4; c++)
+            f(e[c]);
+    };
+    // narrow [lo, hi] to the need-th largest of the keys that are not fixed
+    uint32_t need = static_cast<uint32_t>(p.keep - p.sink - p.recent);
+    for (int pass = 0; need > 0 && lo < hi; pass ^= 1) {
+        int shift = 0;
+        while (((hi - lo) >> shift) >= kBins)
+            shift++;
+        for (int i = tid; i < kBins; i += kThreads)
+            hist[pass][i] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int q = q0 + tid; q < quads; q += kThreads)
+            each4(q, [&](uint32_t k) {
+                if (k >= lo && k <= hi)   // (hi is below kFixed)
+                    atomicAdd(&hist[pass][(k - lo) >> shift], 1u);
+            });
+        cluster.sync();
+        // the bin, counted from the top, in which the running count reaches `need`
+        constexpr int kPer = kBins / kThreads;
+        uint32_t c[kPer], sum = 0;
+        const uint32_t *counts = hist[pass];
+        if (C > 1) {
+            // 4 bins to a lane, each CTA starting at its own neighbour, every load in flight at once: read in
+            // the scan's order and all from rank 0 first, this sum took 30 us a pass
+#pragma unroll
+            for (int i = 4 * tid; i < kBins; i += 4 * kThreads) {
+                uint4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    v[k] = k < C ? *reinterpret_cast<const uint4 *>(cluster.map_shared_rank(&hist[pass][i], (rank + k) & (C - 1)))
+                                 : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int k = 1; k < 8; k++) {
+                    v[0].x += v[k].x;
+                    v[0].y += v[k].y;
+                    v[0].z += v[k].z;
+                    v[0].w += v[k].w;
+                }
+                *reinterpret_cast<uint4 *>(joint + i) = v[0];
+            }
+            __syncthreads();
+            counts = joint;
+        }
+#pragma unroll
+        for (int e = 0; e < kPer; e++) {
+            c[e] = counts[kBins - 1 - (kPer * tid + e)];
+            sum += c[e];
+        }
+        uint64_t total;
+        uint32_t above = static_cast<uint32_t>(cta_scan<kThreads>(sum, warp_sums, total)) - sum;
+#pragma unroll
+        for (int e = 0; e < kPer; e++) {
+            if (above < need && above + c[e] >= need) {
+                sh_bin = kBins - 1 - (kPer * tid + e);
+                sh_need = need - above;
+            }
+            above += c[e];
+        }
+        __syncthreads();
+        need = sh_need;   // of the keys in that bin
+        lo += sh_bin << shift;
+        hi = min(hi, lo + ((1u << shift) - 1));
         __syncthreads();
     }
-    auto key = [&](int i) { return in_smem ? keys[i] : read_key(i); };
-
-    // radix select, 8 bits at a time: `prefix` holds the digits found so far of the want-th largest key
-    uint32_t prefix = 0, need = want;
-    if (want > 0)
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += kSelThreads)
-                hist[i] = 0;
-            __syncthreads();
-            for (int i = tid; i < M; i += kSelThreads) {
-                const uint32_t k = key(i);
-                if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-                    atomicAdd(&hist[(k >> shift) & 255u], 1u);
-            }
-            __syncthreads();
-            if (tid < 32) {
-                // lane holds 8 digits, highest first over the warp: the digit where the running count
-                // from above reaches `need`
-                uint32_t c[8], sum = 0;
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    c[e] = hist[255 - (8 * tid + e)];
-                    sum += c[e];
-                }
-                uint32_t x = sum;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
-                    if (tid >= d)
-                        x += y;
-                }
-                uint32_t above = x - sum;
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    if (above < need && above + c[e] >= need) {
-                        sh_digit = 255 - (8 * tid + e);
-                        sh_need = need - above;
-                    }
-                    above += c[e];
-                }
-            }
-            __syncthreads();
-            prefix |= sh_digit << shift;
-            need = sh_need;   // of the keys that share the digits so far
-            __syncthreads();
-        }
-    // keys above `prefix` stay, and the first `need` that equal it
-    for (int j = tid; j < p.sink; j += kSelThreads)
-        kept[j] = j;
-    for (int j = tid; j < p.recent; j += kSelThreads)
-        kept[p.keep - p.recent + j] = L - p.recent + j;
-    if (want == 0)
-        return;
-    const int per = ((M + kSelThreads - 1) / kSelThreads) | 1;   // odd: no bank conflicts between threads
-    const int i0 = min(M, tid * per), i1 = min(M, i0 + per);
-    uint64_t mine = 0;   // (above, equal) of this thread's run
-    for (int i = i0; i < i1; i++) {
+    // (released here and not at the start: CTAs of the move that only wait would hold the places of
+    // selections still to run, 101 instead of 85 us for 64 x 4096 tokens)
+    pdl_launch_dependents();
+    // keys above `lo` stay, and the first `need` that equal it: a run of tokens per warp, 32 at a time
+    const uint32_t cut = p.keep > p.sink + p.recent ? lo : kFixed - 1;   // nothing to choose: only the fixed
+    const int per = (t1 - t0 + kThreads - 1) / kThreads * 32;
+    const int i0 = min(t1, t0 + (tid >> 5) * per), i1 = min(t1, i0 + per);
+    auto key = [&](int i) -> uint32_t {
+        if (in_smem)
+            return keys[i - t0];
+        const uint4 k = read4(i / 4);
+        return (i & 3) == 0 ? k.x : (i & 3) == 1 ? k.y : (i & 3) == 2 ? k.z : k.w;
+    };
+    uint64_t mine = 0;   // (above, equal) of this lane's tokens
+#pragma unroll 4
+    for (int i = i0 + lane; i < i1; i += 32) {
         const uint32_t k = key(i);
-        mine += (static_cast<uint64_t>(k > prefix) << 32) | (k == prefix);
+        mine += (static_cast<uint64_t>(k > cut) << 32) | (k == cut);
     }
     uint64_t total;
-    const uint64_t incl = cta_scan(mine, warp_sums, total);
-    uint32_t above = static_cast<uint32_t>((incl - mine) >> 32), equal = static_cast<uint32_t>(incl - mine);
-    for (int i = i0; i < i1; i++) {
-        const uint32_t k = key(i);
-        if (k > prefix || (k == prefix && equal < need))
-            kept[p.sink + above + min(equal, need)] = p.sink + i;
-        above += k > prefix;
-        equal += k == prefix;
+    uint64_t first = cta_scan<kThreads>(mine, warp_sums, total) - mine;
+    if (tid == 0)
+        sh_count = total;
+    cluster.sync();
+    for (int r = 0; r < rank; r++)
+        first += *cluster.map_shared_rank(&sh_count, r);
+    first = __shfl_sync(0xFFFFFFFFu, first, 0);   // before this warp's run
+    uint32_t above = static_cast<uint32_t>(first >> 32), equal = static_cast<uint32_t>(first);
+    const uint32_t below = (1u << lane) - 1;
+#pragma unroll 1
+    for (int b = i0; b < i1; b += 128) {
+        uint32_t k[4];
+#pragma unroll
+        for (int c = 0; c < 4; c++)
+            k[c] = b + 32 * c + lane < i1 ? key(b + 32 * c + lane) : 0;
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            const int i = b + 32 * c + lane;
+            const bool gt = i < i1 && k[c] > cut, eq = i < i1 && k[c] == cut;
+            const uint32_t mg = __ballot_sync(0xFFFFFFFFu, gt), me = __ballot_sync(0xFFFFFFFFu, eq);
+            uint32_t q = equal;
+            if (me != 0) {
+                q += __popc(me & below);
+                equal += __popc(me);
+            }
+            if (gt || (eq && q < need))
+                kept[above + __popc(mg & below) + min(q, need)] = i;
+            above += __popc(mg);
+        }
     }
+    if (C > 1)
+        cluster.sync();   // the others may still read this CTA's shared memory
 }
 
 // A warp per (sequence, kv head, new page).
@@ -203,31 +298,47 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictParams p)
     const int pages_per = (p.keep + kPageSize - 1) / kPageSize;
     const int64_t units = static_cast<int64_t>(p.num_seqs) * p.hkv * pages_per;
     const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units; u += step) {
+    // page u's destination row (-1: nothing to do) and, per lane r (and r + 16), the source row of its
+    // kept token r (-1: none), both within one (page, kv head): looked up one page ahead
+    struct Rows {
+        int64_t dst, src;
+    };
+    auto look = [&](int64_t u) -> Rows {
+        Rows x = {-1, -1};
+        if (u >= units)
+            return x;
         const int64_t sh = u / pages_per;
         const int jp = static_cast<int>(u - sh * pages_per);
         const int s = static_cast<int>(sh / p.hkv), h = static_cast<int>(sh - static_cast<int64_t>(s) * p.hkv);
         const int n = min(kPageSize, p.new_lens[s] - kPageSize * jp);
         if (n <= 0)
-            continue;
+            return x;
         const int32_t to = p.new_table[static_cast<int64_t>(s) * p.new_blocks + jp];
-        // lane r (and r + 16): kept token r of the page, as its row within one (page, kv head, half)
-        int64_t src = -1;
+        if (to < 0 || to >= p.num_pages) {
+            if (lane == 0)
+                set_status(p.status, SAW_DEV_BAD_PAGE);
+            return x;
+        }
+        x.dst = (static_cast<int64_t>(to) * p.hkv + h) * (2 * kPageSize);
         const int r16 = lane & 15;
         if (r16 < n) {
             const int32_t t = p.kept[sh * p.keep + kPageSize * jp + r16];
             const int32_t page = p.block_table[static_cast<int64_t>(s) * p.max_blocks + t / kPageSize];
             if (page >= 0 && page < p.num_pages)
-                src = (static_cast<int64_t>(page) * p.hkv + h) * (2 * kPageSize) + t % kPageSize;
+                x.src = (static_cast<int64_t>(page) * p.hkv + h) * (2 * kPageSize) + t % kPageSize;
             else
                 set_status(p.status, SAW_DEV_BAD_PAGE);
         }
-        if (to < 0 || to >= p.num_pages) {
-            if (lane == 0)
-                set_status(p.status, SAW_DEV_BAD_PAGE);
+        return x;
+    };
+    int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    Rows next = look(u);
+    for (; u < units; u += step) {
+        const int64_t src = next.src, dst = next.dst;
+        if (dst < 0) {
+            next = look(u + step);
             continue;
         }
-        const int64_t dst = (static_cast<int64_t>(to) * p.hkv + h) * (2 * kPageSize);
         uint4 w[kSteps];
         bool live[kSteps];
 #pragma unroll
@@ -246,6 +357,7 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictParams p)
             if (lane < 16)
                 m = p.mass[(src / (2 * kPageSize)) * kPageSize + src % (2 * kPageSize)];
         }
+        next = look(u + step);
 #pragma unroll
         for (int i = 0; i < kSteps; i++) {
             const int row = i * kRowsPerStep + lane / kLanes;
@@ -283,31 +395,43 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream)
     p.recent = a.recent;
     p.status = a.status;
     const int64_t most = static_cast<int64_t>(a.max_blocks) * kPageSize;
-    p.smem_keys = static_cast<int32_t>(std::min<int64_t>(most, kSelSmemKeys));
+    const int64_t segments = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
 
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const size_t smem = static_cast<size_t>(p.smem_keys) * 4;
+    // a cluster of up to 8 CTAs per (sequence, kv head) while that fills no more than the SMs and leaves
+    // each CTA a page for every warp; at most 16 tokens a thread: 256 threads, several CTAs to an SM
+    int C = 1;
+    while (C < 8 && 2 * C * segments <= sms && most / (2 * C) >= 512)
+        C *= 2;
+    const int64_t chunk = ((most + C - 1) / C + kPageSize - 1) / kPageSize * kPageSize;
+    p.smem_keys = static_cast<int32_t>(std::min<int64_t>(chunk, kSelSmemKeys));
+    auto *select = chunk <= 4096 ? evict_select_kernel<256> : evict_select_kernel<1024>;
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSelSmemKeys * 4);
+        e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemKeys * 4);
     if (e != cudaSuccess)
         return e;
-    evict_select_kernel<<<static_cast<unsigned>(a.num_seqs * a.num_kv_heads), kSelThreads, smem, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess)
-        return e;
-    const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * ((a.keep + kPageSize - 1) / kPageSize);
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((units + 7) / 8, 8 * sms)));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(static_cast<unsigned>(segments * C));
+    cfg.blockDim = dim3(chunk <= 4096 ? 256 : 1024);
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_keys) * 4;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, select, p)) != cudaSuccess)
+        return e;
+    const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * ((a.keep + kPageSize - 1) / kPageSize);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((units + 7) / 8, 8 * sms)));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
     e = a.head_dim == 64    ? cudaLaunchKernelEx(&cfg, evict_move_kernel<64>, p)
         : a.head_dim == 128 ? cudaLaunchKernelEx(&cfg, evict_move_kernel<128>, p)
                             : cudaLaunchKernelEx(&cfg, evict_move_kernel<256>, p);
