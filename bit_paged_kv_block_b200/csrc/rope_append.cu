@@ -31,21 +31,27 @@ struct RopeTableParams {
     double turns[128];         // f_i / (2 pi): turns per position
 };
 
-// One thread per (position, pair).  The angle in turns is formed in fp64 (position 2^20 at one
-// radian per position keeps 33 bits below the point), reduced to [-1/2, 1/2] exactly and only then
-// rounded to fp32.
+// A thread keeps one pair and takes every rows-th position: the frequency is loaded and the position
+// divided once.  The angle in turns is formed in fp64 (position 2^20 at one radian per position keeps
+// 33 bits below the point), reduced to [-1/2, 1/2] exactly and only then rounded to fp32.  Bound by the
+// writes: 4 R bytes per position (one thread per entry, dividing 64-bit indices, took 5 times as long).
 __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ RopeTableParams p)
 {
-    const int64_t n = p.count * p.half;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t row = i / p.half;
-        const int col = static_cast<int>(i - row * p.half);
-        const double x = static_cast<double>(p.first + row) * p.turns[col];
+    const int rows = 256 / p.half;   // positions a block takes at once
+    const int col = threadIdx.x % p.half, sub = threadIdx.x / p.half;
+    if (sub >= rows)
+        return;
+    const double turns = p.turns[col];
+    const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
+#pragma unroll 2
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows + sub; row < p.count; row += step) {
+        const double x = static_cast<double>(p.first + row) * turns;
         const float r = static_cast<float>(x - rint(x));
         float s, c;
         sincospif(2.0f * r, &s, &c);
-        p.table[row * 2 * p.half + col] = c * p.amplitude;
-        p.table[row * 2 * p.half + p.half + col] = s * p.amplitude;
+        float *out = p.table + row * (2 * p.half) + col;
+        out[0] = c * p.amplitude;
+        out[p.half] = s * p.amplitude;
     }
 }
 
@@ -517,8 +523,8 @@ cudaError_t launch_rope_table(const RopeTableArgs &a, cudaStream_t stream)
     p.amplitude = static_cast<float>(a.amplitude);
     for (int i = 0; i < p.half; i++)
         p.turns[i] = a.turns[i];
-    const int64_t n = p.count * p.half;
-    rope_table_kernel<<<static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 148 * 16)), 256, 0, stream>>>(p);
+    const int64_t rows = 256 / p.half;
+    rope_table_kernel<<<static_cast<unsigned>(std::min<int64_t>((p.count + rows - 1) / rows, 148 * 16)), 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
