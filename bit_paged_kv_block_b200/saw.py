@@ -705,53 +705,43 @@ def rope_scaling(kind: str = "none", base: float = 10000.0, factor: float = 1.0,
 def saw_rope_table(table, scaling: saw_rope_scaling, first_position: int = 0, stream=None) -> None:
     """Fill a rotary table (fp32 [num_positions][rotary_dim]: cosines, then sines), row r for
     position first_position + r."""
-    if table is None:
-        raise TypeError("table must be a torch.Tensor")
+    _present("table", table)
     _need_here((table, "table", torch.float32, 2))
     rc = lib.saw_rope_table(_ptr(table), int(first_position), table.shape[0], table.shape[1],
                             ctypes.byref(scaling), _stream(stream))
     _check(rc, "saw_rope_table")
 
 
-def _rope_desc(rope) -> saw_rope:
-    table, interleaved = rope
-    if table is None:
-        raise TypeError("the rotary table must be a torch.Tensor")
-    _need_here((table, "the rotary table", torch.float32, 2))
-    positions, rotary = table.shape
-    return saw_rope(table.data_ptr(), positions, rotary, 1 if interleaved else 0)
-
-
-def _need_here(*specs) -> None:
-    """_need for (tensor, name, dtype, dimensions) of one call, whose tensors must all be on the
-    current CUDA device: the library launches there."""
-    device = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+def _need_here(*specs) -> int:
+    """_need for (tensor or None, name, dtype, dimensions) of one call, whose tensors must all be on
+    the current CUDA device: the library launches there.  Returns that device."""
+    device = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
     for t, name, dtype, ndim in specs:
         if t is None:
             continue
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.dim() == ndim
-                and t.is_contiguous()):
-            _need(t, name, dtype, ndim)
-        if t.get_device() != device:
-            raise ValueError(f"{name} must be on the current device (cuda:{device}), got {t.device}")
+        if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device \
+                and t.dim() == ndim and t.is_contiguous():
+            continue
+        _need(t, name, dtype, ndim)
+        raise ValueError(f"{name} must be on the current device (cuda:{device}), got {t.device}")
+    return device
 
 
-def _token_rows(t, name: str, tokens: int, heads, d: int) -> int:
+def _token_rows(t, name: str, shape, device: int) -> int:
     """Check a token-strided [T][heads][D] bf16 view on the current device (heads of a token
-    contiguous); its token stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+    contiguous); its token stride, 0 when it is contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be a bf16 tensor")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != device:
         raise ValueError(f"{name} must be on the current CUDA device")
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != tokens or shape[2] != d or (heads is not None and shape[1] != heads):
-        raise ValueError(f"{name} must be [T][heads][{d}] matching the cache, got {tuple(shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} ([T][heads][D]), got {tuple(t.shape)}")
     if t.is_contiguous():
         return 0
     st, sh, se = t.stride()
-    if se != 1 or (shape[1] > 1 and sh != d):
+    if se != 1 or (shape[1] > 1 and sh != shape[2]):
         raise ValueError(f"{name} must have contiguous heads within a token")
-    return st if tokens > 1 else 0
+    return st if shape[0] > 1 else 0
 
 
 @functools.lru_cache(maxsize=256)
@@ -762,12 +752,16 @@ def _cache_desc_of(num_pages: int, hkv: int, two: int, page: int, half: int) -> 
     return saw_cache_desc(hkv, half * 2, page, num_pages)
 
 
-def _cache_checks(kv_pages, scales, dev_status, mass=None):
-    """Check a cache's tensors; its descriptor (shared between calls: not to be changed)."""
-    _need_here((kv_pages, "kv_pages", torch.uint8, 5), (scales, "scales", torch.float16, 5),
-               (mass, "mass", torch.float32, 3), (dev_status, "dev_status", torch.int32, 1))
+def _cache_specs(kv_pages, scales, dev_status, mass=None):
+    """What _need_here checks of a cache's tensors."""
     if kv_pages is None or scales is None:
         raise TypeError("kv_pages and scales must be torch.Tensors")
+    return ((kv_pages, "kv_pages", torch.uint8, 5), (scales, "scales", torch.float16, 5),
+            (mass, "mass", torch.float32, 3), (dev_status, "dev_status", torch.int32, 1))
+
+
+def _cache_of(kv_pages, scales, mass=None):
+    """The descriptor of a checked cache (shared between calls: not to be changed)."""
     pages, hkv, two, page, half = kv_pages.shape
     desc = _cache_desc_of(pages, hkv, two, page, half)
     if scales.shape != (pages, hkv, 2, PAGE_SIZE, 2):
@@ -777,25 +771,30 @@ def _cache_checks(kv_pages, scales, dev_status, mass=None):
     return desc
 
 
-def _rope_checks(q, k, v, positions, slot_mapping, q_out, desc):
-    if positions is None or slot_mapping is None:
-        raise TypeError("positions and slot_mapping must be torch.Tensors")
-    _need_here((positions, "positions", torch.int64, 1), (slot_mapping, "slot_mapping", torch.int64, 1),
-               (q_out, "q_out", torch.bfloat16, 3))
+def _present(names: str, *tensors) -> None:
+    if any(t is None for t in tensors):
+        raise TypeError(f"{names} must be torch.Tensors")
+
+
+def _rope_rows(q, k, v, positions, slot_mapping, q_out, rope, desc, device):
+    """Check one append's rows; (T, Hq, strides of q, k and v, the rotary descriptor)."""
     T = slot_mapping.shape[0]
     if positions.shape[0] != T:
         raise ValueError("positions and slot_mapping must have one entry per token")
-    hkv, d = desc.num_kv_heads, desc.head_dim
-    ks = _token_rows(k, "k", T, hkv, d)
-    vs = _token_rows(v, "v", T, hkv, d)
-    if q is None or q_out is None:
-        if q is not q_out:
-            raise ValueError("q and q_out go together")
-        return T, 0, 0, ks, vs
-    qs = _token_rows(q, "q", T, None, d)
-    if q_out.shape != q.shape:
-        raise ValueError("q_out must be shaped as q")
-    return T, q.shape[1], qs, ks, vs
+    shape = (T, desc.num_kv_heads, desc.head_dim)
+    ks, vs = _token_rows(k, "k", shape, device), _token_rows(v, "v", shape, device)
+    hq = qs = 0
+    if q is not None and q_out is not None:
+        shape = q_out.shape
+        if shape[0] != T or shape[2] != desc.head_dim:
+            raise ValueError(f"q_out must be [T][Hq][{desc.head_dim}] matching the cache")
+        qs, hq = _token_rows(q, "q", shape, device), shape[1]
+    elif q is not q_out:
+        raise ValueError("q and q_out go together")
+    table, interleaved = rope
+    num_positions, rotary = table.shape
+    return T, hq, qs, ks, vs, saw_rope(table.data_ptr(), num_positions, rotary,
+                                       1 if interleaved else 0)
 
 
 def allocate_mass(num_pages: int, num_kv_heads: int, device="cuda") -> torch.Tensor:
@@ -809,9 +808,14 @@ def saw_rope_rotate_quantize_paged(q, k, v, positions, slot_mapping, rope, q_out
     with rope = (table, interleaved), write q to q_out, and rotate, quantize and scatter k and v
     into the cache; mass, when given, is set to 0 at the new slots.  q = q_out = None appends keys
     alone.  rotate=False writes a plain INT4 cache."""
-    desc = _cache_checks(kv_pages, scales, dev_status, mass)
-    rp = _rope_desc(rope)
-    T, hq, qs, ks, vs = _rope_checks(q, k, v, positions, slot_mapping, q_out, desc)
+    _present("positions, slot_mapping and the rotary table", positions, slot_mapping, rope[0])
+    device = _need_here(*_cache_specs(kv_pages, scales, dev_status, mass),
+                        (positions, "positions", torch.int64, 1),
+                        (slot_mapping, "slot_mapping", torch.int64, 1),
+                        (q_out, "q_out", torch.bfloat16, 3),
+                        (rope[0], "the rotary table", torch.float32, 2))
+    desc = _cache_of(kv_pages, scales, mass)
+    T, hq, qs, ks, vs, rp = _rope_rows(q, k, v, positions, slot_mapping, q_out, rope, desc, device)
     fn = lib.saw_rope_rotate_quantize_paged if rotate else lib.saw_rope_quantize_paged_plain
     rc = fn(ctypes.byref(desc), ctypes.byref(rp), hq, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
             _ptr(positions), _ptr(slot_mapping), T, _ptr(q_out), _ptr(kv_pages), _ptr(scales),
@@ -837,19 +841,21 @@ def allocate_prefix_workspace(num_kv_heads: int, num_q_heads: int, num_seqs: int
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _decode_bf16_out_checks(q, block_table, seq_lens, out, workspace, desc):
-    if q is None or out is None or block_table is None or seq_lens is None or workspace is None:
-        raise TypeError("q, block_table, seq_lens, out and workspace must be torch.Tensors")
-    _need_here((q, "q", torch.bfloat16, 3), (out, "out", torch.bfloat16, 3),
-               (block_table, "block_table", torch.int32, 2), (seq_lens, "seq_lens", torch.int32, 1),
-               (workspace, "workspace", torch.uint8, 1))
+def _decode_bf16_out(q, kv_pages, scales, block_table, seq_lens, out, workspace, dev_status, mass,
+                     *more):
+    """Check a decode that writes bf16 rows; (descriptor, S, Hq)."""
+    _present("q, block_table, seq_lens, out and workspace", q, block_table, seq_lens, out, workspace)
+    _need_here(*_cache_specs(kv_pages, scales, dev_status, mass), (q, "q", torch.bfloat16, 3),
+               (out, "out", torch.bfloat16, 3), (block_table, "block_table", torch.int32, 2),
+               (seq_lens, "seq_lens", torch.int32, 1), (workspace, "workspace", torch.uint8, 1), *more)
+    desc = _cache_of(kv_pages, scales, mass)
     shape = q.shape
     S, hq, d = shape
     if d != desc.head_dim or out.shape != shape:
         raise ValueError(f"q and out must be [S][Hq][{desc.head_dim}] matching the cache")
     if block_table.shape[0] != S or seq_lens.shape[0] != S:
         raise ValueError("block_table and seq_lens need one row per sequence")
-    return S, hq
+    return desc, S, hq
 
 
 def saw_paged_decode_attn_prefix(q, kv_pages, scales, prefix_table, prefix_len, block_table,
@@ -858,10 +864,9 @@ def saw_paged_decode_attn_prefix(q, kv_pages, scales, prefix_table, prefix_len, 
     """Decode attention of q (bf16 [S][Hq][D]) over a prefix that all sequences share (prefix_len
     tokens in the pages of prefix_table, int32) and then each sequence's own seq_lens tokens, one
     softmax over both, into out (bf16 [S][Hq][D])."""
-    desc = _cache_checks(kv_pages, scales, dev_status)
-    S, hq = _decode_bf16_out_checks(q, block_table, seq_lens, out, workspace, desc)
+    desc, S, hq = _decode_bf16_out(q, kv_pages, scales, block_table, seq_lens, out, workspace,
+                                   dev_status, None, (prefix_table, "prefix_table", torch.int32, 1))
     prefix_len = int(prefix_len)
-    _need_here((prefix_table, "prefix_table", torch.int32, 1))
     if prefix_len > PAGE_SIZE * (0 if prefix_table is None else prefix_table.shape[0]):
         raise ValueError("prefix_table must hold a page for every 16 prefix tokens")
     if sm_scale is None:
@@ -896,10 +901,9 @@ def saw_paged_decode_attn_mass(q, kv_pages, scales, mass, block_table, seq_lens,
     """Decode attention of q (bf16 [S][Hq][D]) into out (bf16 [S][Hq][D]) that also adds every
     cached token's attention weight, summed over the query heads of its kv head, to mass (fp32
     [num_pages][Hkv][16])."""
-    if mass is None:
-        raise TypeError("mass must be a torch.Tensor")
-    desc = _cache_checks(kv_pages, scales, dev_status, mass)
-    S, hq = _decode_bf16_out_checks(q, block_table, seq_lens, out, workspace, desc)
+    _present("mass", mass)
+    desc, S, hq = _decode_bf16_out(q, kv_pages, scales, block_table, seq_lens, out, workspace,
+                                   dev_status, mass)
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(desc.head_dim)
     fn = lib.saw_paged_decode_attn_mass if rotate else lib.saw_paged_decode_attn_mass_plain
@@ -915,14 +919,13 @@ def saw_evict_paged(kv_pages, scales, mass, block_table, seq_lens, new_table, ne
     `recent` and the heaviest between them (mass) move, in order, into the pages of new_table
     (int32 [S][blocks]); new_lens (int32 [S]) and kept (int32 [S][Hkv][keep], old indices, -1 past
     new_lens) are written.  The old pages are only read."""
-    if mass is None:
-        raise TypeError("mass must be a torch.Tensor")
-    desc = _cache_checks(kv_pages, scales, dev_status, mass)
-    if any(t is None for t in (block_table, seq_lens, new_table, new_lens, kept)):
-        raise TypeError("block_table, seq_lens, new_table, new_lens and kept must be torch.Tensors")
-    _need_here((block_table, "block_table", torch.int32, 2), (seq_lens, "seq_lens", torch.int32, 1),
+    _present("mass, block_table, seq_lens, new_table, new_lens and kept", mass, block_table, seq_lens,
+             new_table, new_lens, kept)
+    _need_here(*_cache_specs(kv_pages, scales, dev_status, mass),
+               (block_table, "block_table", torch.int32, 2), (seq_lens, "seq_lens", torch.int32, 1),
                (new_table, "new_table", torch.int32, 2), (new_lens, "new_lens", torch.int32, 1),
                (kept, "kept", torch.int32, 3))
+    desc = _cache_of(kv_pages, scales, mass)
     S = seq_lens.shape[0]
     if block_table.shape[0] != S or new_table.shape[0] != S or new_lens.shape[0] != S:
         raise ValueError("block_table, new_table and new_lens need one row per sequence")
@@ -943,21 +946,27 @@ def saw_decode_step_rope(q, k_new, v_new, positions, slot_mapping, rope, q_rot, 
     saw_rope_rotate_quantize_paged (q to q_rot), then the decode.  Without mass:
     saw_paged_decode_attn (out fp32, its workspace); with mass: saw_paged_decode_attn_mass (out
     bf16, its workspace)."""
-    desc = _cache_checks(kv_pages, scales, dev_status, mass)
-    rp = _rope_desc(rope)
-    for t, name in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
-        _need(t, name, torch.bfloat16, 3)
-    _rope_checks(q, k_new, v_new, positions, slot_mapping, q_rot, desc)
+    _present("q, q_rot, positions, slot_mapping and the rotary table", q, q_rot, positions,
+             slot_mapping, rope[0])
+    device = _need_here(*_cache_specs(kv_pages, scales, dev_status, mass),
+                        (q, "q", torch.bfloat16, 3), (k_new, "k_new", torch.bfloat16, 3),
+                        (v_new, "v_new", torch.bfloat16, 3), (q_rot, "q_rot", torch.bfloat16, 3),
+                        (positions, "positions", torch.int64, 1),
+                        (slot_mapping, "slot_mapping", torch.int64, 1),
+                        (rope[0], "the rotary table", torch.float32, 2))
+    desc = _cache_of(kv_pages, scales, mass)
+    rp = _rope_rows(q, k_new, v_new, positions, slot_mapping, q_rot, rope, desc, device)[-1]
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(desc.head_dim)
     head = (ctypes.byref(desc), ctypes.byref(rp), q.shape[1], _ptr(q), _ptr(k_new), _ptr(v_new),
             _ptr(positions), _ptr(slot_mapping), _ptr(q_rot), _ptr(kv_pages), _ptr(scales))
     if mass is None:
-        S, _ = _decode_checks(q_rot, kv_pages, scales, block_table, seq_lens, out, workspace,
-                              dev_status)[1:]
+        S = _decode_checks(q_rot, kv_pages, scales, block_table, seq_lens, out, workspace,
+                           dev_status)[1]
         fn, name = lib.saw_decode_step_rope, "saw_decode_step_rope"
     else:
-        S, _ = _decode_bf16_out_checks(q_rot, block_table, seq_lens, out, workspace, desc)
+        S = _decode_bf16_out(q_rot, kv_pages, scales, block_table, seq_lens, out, workspace, dev_status,
+                             mass)[1]
         head += (_ptr(mass),)
         fn, name = lib.saw_decode_step_rope_mass, "saw_decode_step_rope_mass"
     rc = fn(*head, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), S, float(sm_scale),
