@@ -475,6 +475,26 @@ __device__ __forceinline__ void copy_page_elected(uint32_t bar, uint32_t dst_cod
 }
 
 
+// copy_page_elected with an L2 policy that evicts the page first: pages are read once, and a kernel that
+// writes what the next one reads (the logits of the decode with accumulated weights) keeps L2 for it.
+template <int kD>
+__device__ __forceinline__ void copy_page_once_elected(uint32_t bar, uint32_t dst_codes, const void *tmap,
+                                                       int32_t row, uint32_t dst_scales,
+                                                       const void *src_scales)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 pol;\n\t"
+                 "createpolicy.fractional.L2::evict_first.b64 pol, 1.0;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "@p mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %6;\n\t"
+                 "@p cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+                 " [%1], [%2, {%7, %3}], [%0], pol;\n\t"
+                 "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+                 " [%4], [%5], %8, [%0], pol;\n\t"
+                 "}"
+                 ::"r"(bar), "r"(dst_codes), "l"(tmap), "r"(row), "r"(dst_scales), "l"(src_scales),
+                 "r"(static_cast<uint32_t>(code_bytes(kD) + kScaleBytes)), "r"(0), "r"(static_cast<uint32_t>(kScaleBytes))
+                 : "memory");
+}
 
 // The INT4 page format for the generic decode kernel (decode_common.cuh), head dimension kD:
 // 4 warps per CTA and a ring per warp whose stages hold the codes of one (page, kv head) (32
@@ -513,8 +533,12 @@ struct Int4Format {
     __device__ static void issue(const Ring &r, int stg, uint32_t bar, const CUtensorMap *tmap,
                                  int32_t row, const DecodeParams &p)
     {
-        copy_page_elected<kD>(bar, r.code0 + stg * kCodeBytes, tmap, row,
-                              r.scale0 + stg * kScaleBytes, p.scales + static_cast<int64_t>(row) * 4);
+        if constexpr (kRole == kRoleMass)
+            copy_page_once_elected<kD>(bar, r.code0 + stg * kCodeBytes, tmap, row,
+                                       r.scale0 + stg * kScaleBytes, p.scales + static_cast<int64_t>(row) * 4);
+        else
+            copy_page_elected<kD>(bar, r.code0 + stg * kCodeBytes, tmap, row,
+                                  r.scale0 + stg * kScaleBytes, p.scales + static_cast<int64_t>(row) * 4);
     }
     __device__ static void load_query(const DecodeParams &p, uint32_t qbuf, int nheads, int lane,
                                       Query &q)
