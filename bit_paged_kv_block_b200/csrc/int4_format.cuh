@@ -49,13 +49,22 @@ constexpr int kRoleDecode = 0;   // decode and chunked prefill
 constexpr int kRoleWindow = 1;   // the quantized part of a windowed decode
 constexpr int kRoleMass = 2;     // decode with accumulated attention weights
 constexpr int kRolePrefix = 3;   // shared-prefix decode
+constexpr int kRoleMass4 = 4;    // kRoleMass for at most 4 query heads per kv head
+
+// How the logits reach fp32's accuracy: not at all; by a second MMA chain over the low parts of the
+// query; or, with at most 4 query heads, by the same MMA: its columns 4 .. 7 hold the low parts of
+// heads 0 .. 3, and adding the halves leaves every head's logits in two columns, which from there on are
+// two copies of one row.  (The second chain costs 11 us of 96 at 64 x 8192 tokens.)
+constexpr int kSplitNone = 0;
+constexpr int kSplitChain = 1;
+constexpr int kSplitColumns = 2;
 
 // One segment's query: B fragments, per-column sums, and (kSplit) the low parts and where this
 // step's logits go.
-template <int kD, bool kSplit>
+template <int kD, int kSplit>
 struct QueryFragments {
     uint32_t bq[kD / 16][2];
-    uint32_t lo[kSplit ? kD / 16 : 1][2];   // 2^11 (q - fp16(q)), fp16
+    uint32_t lo[kSplit == kSplitChain ? kD / 16 : 1][2];   // 2^11 (q - fp16(q)), fp16
     float sq[2];
     float *logits;                          // [16 tokens][rows] of the next page
     int rows;
@@ -67,19 +76,20 @@ constexpr float kLowPart = 2048.0f;         // 2^11: keeps the low parts in fp16
 // Thread (g, t) owns query head g of the group and d in [kQ t, kQ t + kQ), kQ = kD / 4.  The
 // rotation is the Hadamard transform of each block of B = min(kD, 128) elements of d (for
 // kD = 256 the two halves are independent blocks, as the quantizer rotates them).
-// kSplit: the query enters as fp16 high and low parts, 22 significant bits together, so that the
-// logits keep fp32's accuracy (the codes are exact); sum(q) is then the fp32 sum.
-template <bool kRotate, int kD, bool kSplit>
+// kSplit (other than none): the query enters as fp16 high and low parts, 22 significant bits together, so
+// that the logits keep fp32's accuracy (the codes are exact); sum(q) is then the fp32 sum.
+template <bool kRotate, int kD, int kSplit>
 __device__ __forceinline__ void load_query(const DecodeParams &p, uint32_t qbuf, int nheads, int g,
                                            int t, QueryFragments<kD, kSplit> &out)
 {
     constexpr int kQ = kD / 4;
     constexpr int kBlock = kD < 128 ? kD : 128;
     float x[kQ];
-    if (g < nheads) {
+    const int row = kSplit == kSplitColumns ? g & 3 : g;
+    if (row < nheads) {
 #pragma unroll
         for (int c = 0; c < kQ / 8; c++) {
-            const uint4 u = lds128(qbuf + g * (kD * 2) + 2 * kQ * t + 16 * c);
+            const uint4 u = lds128(qbuf + row * (kD * 2) + 2 * kQ * t + 16 * c);
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int k = 0; k < 4; k++) {
@@ -122,9 +132,11 @@ __device__ __forceinline__ void load_query(const DecodeParams &p, uint32_t qbuf,
         const float qv = x[l] * p.q_mult;
         const float qs = (l & 1) ? qv * 0.0625f : qv;
         hq[l] = __float2half_rn(qs);
-        if constexpr (kSplit) {
+        if constexpr (kSplit != kSplitNone) {
             x[l] = (qs - __half2float(hq[l])) * kLowPart;   // the difference is exact
             sq += qv;
+            if (kSplit == kSplitColumns && g >= 4)
+                hq[l] = __float2half_rn(x[l]);
         } else {
             sq += (l & 1) ? 16.0f * __half2float(hq[l]) : __half2float(hq[l]);
         }
@@ -139,7 +151,7 @@ __device__ __forceinline__ void load_query(const DecodeParams &p, uint32_t qbuf,
             const int l0 = 8 * i + 2 * e;
             out.bq[2 * i + e][0] = half2_as_u32(__halves2half2(hq[l0], hq[l0 + 4]));
             out.bq[2 * i + e][1] = half2_as_u32(__halves2half2(hq[l0 + 1], hq[l0 + 5]));
-            if constexpr (kSplit) {
+            if constexpr (kSplit == kSplitChain) {
                 out.lo[2 * i + e][0] = half2_as_u32(__floats2half2_rn(x[l0], x[l0 + 4]));
                 out.lo[2 * i + e][1] = half2_as_u32(__floats2half2_rn(x[l0 + 1], x[l0 + 5]));
             }
@@ -163,7 +175,7 @@ __device__ __forceinline__ uint32_t code_offset(int r, int c)
 // s = scale * acc + zero * sum(q) per (token, query column); tokens a column may not see get
 // -inf.  kMask: tokens [0, mask.valid) of the page exist and column e (block row 2t + e) sees
 // tokens [0, mask.col[e]).
-template <bool kMask, int kD, bool kSplit>
+template <bool kMask, int kD, int kSplit>
 __device__ __forceinline__ void page_logits(uint32_t cbase, uint32_t sbase, const PageMask &mask,
                                             const QueryFragments<kD, kSplit> &q, int lane, float s[4])
 {
@@ -209,15 +221,22 @@ __device__ __forceinline__ void page_logits(uint32_t cbase, uint32_t sbase, cons
         const uint32_t a1[4] = {ya[2], yb[2], ya[3], yb[3]};
         mma_16816(acc, a0, q.bq[2 * w][0], q.bq[2 * w][1]);
         mma_16816(acc, a1, q.bq[2 * w + 1][0], q.bq[2 * w + 1][1]);
-        if constexpr (kSplit) {
+        if constexpr (kSplit == kSplitChain) {
             mma_16816(low, a0, q.lo[2 * w][0], q.lo[2 * w][1]);
             mma_16816(low, a1, q.lo[2 * w + 1][0], q.lo[2 * w + 1][1]);
         }
     }
-    if constexpr (kSplit) {
+    if constexpr (kSplit == kSplitChain) {
 #pragma unroll
         for (int k = 0; k < 4; k++)
             acc[k] = fmaf(low[k], 1.0f / kLowPart, acc[k]);
+    }
+    if constexpr (kSplit == kSplitColumns) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const float v = t < 2 ? acc[k] : acc[k] * (1.0f / kLowPart);
+            acc[k] = v + __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+        }
     }
 
     const float2 ksz0 = h2_to_f2(lds32(sbase + 4 * g));
@@ -240,7 +259,7 @@ __device__ __forceinline__ void page_logits(uint32_t cbase, uint32_t sbase, cons
 }
 
 // Store one page's logits as [16 tokens][rows]: tokens g, g + 8 of columns 2t, 2t + 1 (< rows).
-template <int kD, bool kSplit>
+template <int kD, int kSplit>
 __device__ __forceinline__ void store_logits(const QueryFragments<kD, kSplit> &q, float *dst, int lane,
                                              const float s[4])
 {
@@ -310,14 +329,14 @@ __device__ __forceinline__ void page_pv(uint32_t cbase, uint32_t sbase, const Pa
 }
 
 // One page of one warp: QK^T, online softmax, PV.
-template <bool kMask, int kD, bool kSplit>
+template <bool kMask, int kD, int kSplit>
 __device__ __forceinline__ void process_page(uint32_t cbase, uint32_t sbase, const PageMask &mask,
                                              const QueryFragments<kD, kSplit> &q, int lane,
                                              WarpState<kD / 16> &st)
 {
     float s[4], pr[4];
     page_logits<kMask, kD>(cbase, sbase, mask, q, lane, s);
-    if constexpr (kSplit)
+    if constexpr (kSplit != kSplitNone)
         store_logits(q, q.logits, lane, s);
     softmax_update<kMask, kD / 16, 4>(s, st, pr);
     page_pv<kMask, kD>(cbase, sbase, mask, pr, lane, st);
@@ -325,7 +344,7 @@ __device__ __forceinline__ void process_page(uint32_t cbase, uint32_t sbase, con
 
 // Two whole pages of one warp as one step: both pages' logits (two independent tensor-core
 // chains), one online-softmax update over their 32 tokens, then PV for both.
-template <int kD, bool kSplit>
+template <int kD, int kSplit>
 __device__ __forceinline__ void process_pages2(uint32_t cbase0, uint32_t sbase0, uint32_t cbase1,
                                                uint32_t sbase1, const QueryFragments<kD, kSplit> &q,
                                                int lane, WarpState<kD / 16> &st)
@@ -334,7 +353,7 @@ __device__ __forceinline__ void process_pages2(uint32_t cbase0, uint32_t sbase0,
     float s[8], pr[8];
     page_logits<false, kD>(cbase0, sbase0, whole, q, lane, s);
     page_logits<false, kD>(cbase1, sbase1, whole, q, lane, s + 4);
-    if constexpr (kSplit) {
+    if constexpr (kSplit != kSplitNone) {
         store_logits(q, q.logits, lane, s);
         store_logits(q, q.logits + kPageSize * q.rows, lane, s + 4);
     }
@@ -423,7 +442,7 @@ __device__ __forceinline__ void finalize(const DecodeParams &p, const Seg &sg, i
         if (head < sg.nrows) {
             const int64_t off = sg.row_offset(p, head, kD);
             float f = kRotate ? hadamard_c(kD) : 1.0f, fw = 0.0f;
-            if constexpr (kRole == kRoleMass) {
+            if constexpr (kRole == kRoleMass || kRole == kRoleMass4) {
                 store_bf16_row<kD>(p.out_bf16 + off, g, v[e], f);
                 if (g == 0)
                     p.lse[off / kD] = m[e] + log2f(l[e]);
@@ -512,19 +531,23 @@ template <bool kRotate, int kD, int kRole = kRoleDecode>
 struct Int4Format {
     static_assert(kD == 64 || kD == 128 || kD == 256, "head dimension");
     static constexpr int kDim = kD;
-    static constexpr bool kLogits = kRole == kRoleMass;
-    static constexpr bool kRowPieces = kRole == kRoleMass || kRole == kRolePrefix;
+    static constexpr int kSplit = kRole == kRoleMass ? kSplitChain : kRole == kRoleMass4 ? kSplitColumns : kSplitNone;
+    static constexpr bool kLogits = kSplit != kSplitNone;
+    static constexpr bool kRowPieces = kLogits || kRole == kRolePrefix;
     static constexpr int kTiles = kD / 16;
     static constexpr int kWarps = 4;
     static constexpr int kStages = kD == 256 ? 2 : 4;
-    static constexpr int kMinBlocks = kD == 64 ? 5 : kD == 128 ? 4 : kRole == kRoleMass ? 2 : 3;
+    static constexpr int kMinBlocks = kRole == kRoleMass ? (kD == 256 ? 2 : kD == 128 ? 3 : 4)
+                                      : kD == 64       ? 5
+                                      : kD == 128      ? 4
+                                                       : 3;
     static constexpr int kRowsPerPage = 32;
     static constexpr int kCodeBytes = code_bytes(kD);
     static constexpr int kRingBytes = kWarps * kStages * (kCodeBytes + kScaleBytes);
     struct Ring {
         uint32_t code0, scale0;
     };
-    using Query = QueryFragments<kD, kLogits>;
+    using Query = QueryFragments<kD, kSplit>;
     __device__ static Ring ring(uint32_t base, int warp)
     {
         return {base + warp * kStages * kCodeBytes,
@@ -533,7 +556,7 @@ struct Int4Format {
     __device__ static void issue(const Ring &r, int stg, uint32_t bar, const CUtensorMap *tmap,
                                  int32_t row, const DecodeParams &p)
     {
-        if constexpr (kRole == kRoleMass)
+        if constexpr (kLogits)
             copy_page_once_elected<kD>(bar, r.code0 + stg * kCodeBytes, tmap, row,
                                        r.scale0 + stg * kScaleBytes, p.scales + static_cast<int64_t>(row) * 4);
         else
@@ -543,7 +566,7 @@ struct Int4Format {
     __device__ static void load_query(const DecodeParams &p, uint32_t qbuf, int nheads, int lane,
                                       Query &q)
     {
-        saw::load_query<kRotate, kD, kLogits>(p, qbuf, nheads, lane >> 2, lane & 3, q);
+        saw::load_query<kRotate, kD, kSplit>(p, qbuf, nheads, lane >> 2, lane & 3, q);
         q.rows = p.qrows;
     }
     template <bool kMask>

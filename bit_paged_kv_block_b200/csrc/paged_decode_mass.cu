@@ -115,24 +115,26 @@ __global__ void __launch_bounds__(kMassThreads) mass_accumulate_kernel(const Mas
     }
 }
 
-template <bool kRotate, int kD>
-using MassFormat = Int4Format<kRotate, kD, kRoleMass>;
+// The page format for G query heads per kv head: the query's low parts in spare MMA columns up to 4.
+template <bool kRotate, int kD, bool kFew>
+using MassFormat = Int4Format<kRotate, kD, kFew ? kRoleMass4 : kRoleMass>;
+constexpr int kFewHeads = 4;
 
-template <int kD>
+template <int kD, bool kFew>
 cudaError_t mass_shape(size_t smem, size_t merge_smem, LaunchShape &out)
 {
     static ShapeCache shapes;
     static const void *const decode_kernels[kShapeVariants] = {
-        reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<true, kD>, kModeDecode>),
-        reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<false, kD>, kModeDecode>),
-        reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<true, kD>, kModeDecode>),
-        reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<false, kD>, kModeDecode>)};
+        reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<true, kD, kFew>, kModeDecode>),
+        reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<false, kD, kFew>, kModeDecode>),
+        reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<true, kD, kFew>, kModeDecode>),
+        reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<false, kD, kFew>, kModeDecode>)};
     static const void *const merge_kernels[kShapeVariants] = {
         reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModeDecode>),
         reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModeDecode>),
         reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModeDecode>),
         reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModeDecode>)};
-    return decode::launch_shape(shapes, decode_kernels, merge_kernels, 32 * MassFormat<true, kD>::kWarps,
+    return decode::launch_shape(shapes, decode_kernels, merge_kernels, 32 * MassFormat<true, kD, kFew>::kWarps,
                                 smem, merge_smem, out);
 }
 
@@ -145,10 +147,11 @@ template <int kD>
 cudaError_t mass_workspace(int32_t hkv, int32_t hq, int32_t num_seqs, int32_t max_blocks, LaunchShape &ls,
                            MassWorkspace &w)
 {
-    using Fmt = MassFormat<true, kD>;
+    using Fmt = MassFormat<true, kD, false>;   // the layout is the same for all variants
     const int32_t qrows = query_rows(hkv, hq, false);
-    const cudaError_t e = mass_shape<kD>(decode_smem_bytes<Fmt>(num_seqs, qrows),
-                                         row_merge_smem(num_seqs), ls);
+    const size_t smem = decode_smem_bytes<Fmt>(num_seqs, qrows);
+    const cudaError_t e = hq / hkv <= kFewHeads ? mass_shape<kD, true>(smem, row_merge_smem(num_seqs), ls)
+                                                : mass_shape<kD, false>(smem, row_merge_smem(num_seqs), ls);
     if (e != cudaSuccess)
         return e;
     const int64_t segments = max_segments(hkv, hq, num_seqs, 0, false);
@@ -159,10 +162,10 @@ cudaError_t mass_workspace(int32_t hkv, int32_t hq, int32_t num_seqs, int32_t ma
     return cudaSuccess;
 }
 
-template <bool kRotate, int kD>
-cudaError_t launch(const DecodeArgs &a, float *mass, cudaStream_t stream, bool programmatic)
+template <bool kRotate, int kD, bool kFew>
+cudaError_t launch_format(const DecodeArgs &a, float *mass, cudaStream_t stream, bool programmatic)
 {
-    using Fmt = MassFormat<kRotate, kD>;
+    using Fmt = MassFormat<kRotate, kD, kFew>;
     const CUtensorMap *map = code_tensor_map<kD>(a.kv_pages, a.num_pages * a.num_kv_heads * 32);
     if (map == nullptr)
         return cudaErrorInvalidValue;
@@ -211,6 +214,14 @@ cudaError_t launch(const DecodeArgs &a, float *mass, cudaStream_t stream, bool p
     if (e != cudaSuccess)
         return e;
     return cudaGetLastError();
+}
+
+template <bool kRotate, int kD>
+cudaError_t launch(const DecodeArgs &a, float *mass, cudaStream_t stream, bool programmatic)
+{
+    return a.num_q_heads / a.num_kv_heads <= kFewHeads
+               ? launch_format<kRotate, kD, true>(a, mass, stream, programmatic)
+               : launch_format<kRotate, kD, false>(a, mass, stream, programmatic);
 }
 
 }  // namespace
