@@ -130,10 +130,10 @@ cudaError_t mass_shape(size_t smem, size_t merge_smem, LaunchShape &out)
         reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<true, kD, kFew>, kModeDecode>),
         reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<false, kD, kFew>, kModeDecode>)};
     static const void *const merge_kernels[kShapeVariants] = {
-        reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModeDecode>),
-        reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModeDecode>),
-        reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModeDecode>),
-        reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModeDecode>)};
+        reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModeDecode, false>),
+        reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModeDecode, false>),
+        reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModeDecode, true>),
+        reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModeDecode, true>)};
     return decode::launch_shape(shapes, decode_kernels, merge_kernels, 32 * MassFormat<true, kD, kFew>::kWarps,
                                 smem, merge_smem, out);
 }
@@ -156,7 +156,8 @@ cudaError_t mass_workspace(int32_t hkv, int32_t hq, int32_t num_seqs, int32_t ma
         return e;
     const int64_t segments = max_segments(hkv, hq, num_seqs, 0, false);
     auto round = [](size_t n) { return (n + 255) / 256 * 256; };
-    w.lse = round(workspace_bytes_for<Fmt::kTiles>(static_cast<size_t>(ls.sms) * ls.occ * Fmt::kWarps, segments));
+    w.lse = round(hq / hkv <= kFewHeads ? row_slots_bytes<MassFormat<true, kD, true>>(ls, segments)
+                                        : row_slots_bytes<Fmt>(ls, segments));
     w.logits = w.lse + round(static_cast<size_t>(num_seqs) * hq * sizeof(float));
     w.total = w.logits + static_cast<size_t>(segments) * max_blocks * kPageSize * qrows * sizeof(float);
     return cudaSuccess;
@@ -179,7 +180,8 @@ cudaError_t launch_format(const DecodeArgs &a, float *mass, cudaStream_t stream,
     fill_decode_params<kD>(a, p);
     p.qrows = query_rows(a.num_kv_heads, a.num_q_heads, false);
     p.max_segments = max_segments(a.num_kv_heads, a.num_q_heads, a.num_seqs, 0, false);
-    p.total_warps = ls.sms * ls.occ * Fmt::kWarps;
+    const int32_t grid = row_grid<Fmt>(ls, p.max_segments * (a.max_blocks + kKappa));
+    p.total_warps = grid * Fmt::kWarps;
     p.lse = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + w.lse);
     p.logits = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + w.logits);
     mp.mass = mass;
@@ -188,7 +190,7 @@ cudaError_t launch_format(const DecodeArgs &a, float *mass, cudaStream_t stream,
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ls.sms * ls.occ));
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(32 * Fmt::kWarps);
     cfg.dynamicSmemBytes = decode_smem_bytes<Fmt>(a.num_seqs, p.qrows);
     cfg.stream = stream;
@@ -198,14 +200,12 @@ cudaError_t launch_format(const DecodeArgs &a, float *mass, cudaStream_t stream,
     if (e != cudaSuccess)
         return e;
 
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(p.max_segments, 16 * ls.sms)));
-    cfg.blockDim = dim3(32 * kRowWarps);
-    cfg.dynamicSmemBytes = row_merge_smem(a.num_seqs);
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, row_merge_kernel<kRotate, kD, kModeDecode>, p, PrefixPieces{nullptr, 0, 0});
+    e = launch_row_merge<kRotate, kD, kModeDecode>(p, PrefixPieces{nullptr, 0, 0}, ls, p.max_segments, p.max_segments,
+                                                   row_merge_smem(a.num_seqs), stream);
     if (e != cudaSuccess)
         return e;
 
+    cfg.numAttrs = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(4 * ls.sms));
     cfg.blockDim = dim3(kMassThreads);
     cfg.dynamicSmemBytes = mass_smem_bytes(a.num_seqs);

@@ -13,7 +13,7 @@
 // prefix's pages.  All pieces go to workspace slots as rows ([8][D] fp32, then m[8] and l[8]), since
 // the rows of an output segment (sequence, kv head, up to 8 heads) may lie in two blocks of the prefix.
 //
-// At D = 128 and from kTensorRows query rows per kv head on, the prefix is instead a kernel of its own on
+// At D = 128, a prefix with enough query rows and tokens (kTensorRows, kTensorWork) is instead a kernel of its own on
 // the 5th-generation tensor cores (prefix_tc.cu), which the decode kernel over the own tokens runs
 // beside as its programmatic dependent, and the merge joins both kernels' pieces.
 #include <algorithm>
@@ -44,16 +44,21 @@ cudaError_t prefix_shape(size_t smem, size_t merge_smem, LaunchShape &out)
         reinterpret_cast<const void *>(paged_decode_kernel<PrefixFormat<true, kD>, kModePrefix>),
         reinterpret_cast<const void *>(paged_decode_kernel<PrefixFormat<false, kD>, kModePrefix>)};
     static const void *const merge_kernels[kShapeVariants] = {
-        reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModePrefix>),
-        reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModePrefix>),
-        reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModePrefix>),
-        reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModePrefix>)};
+        reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModePrefix, false>),
+        reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModePrefix, false>),
+        reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModePrefix, true>),
+        reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModePrefix, true>)};
     return decode::launch_shape(shapes, decode_kernels, merge_kernels, 32 * PrefixFormat<true, kD>::kWarps,
                                 smem, merge_smem, out);
 }
 
-// The fewest query rows per kv head (S G) that take the prefix to the tensor cores.
-constexpr int64_t kTensorRows = 24;
+// The prefix goes to the tensor cores from 64 query rows per kv head and 2^20 (kv head, row, token) triples
+// on.  Measured with own tokens of 32 - 96 (us, tensor cores / plan): 8 kv heads, 64 rows: 2048 tokens 20.0 /
+// 24.4, 8192 24.8 / 34.9; 128 rows: 512 tokens 17.6 / 17.3, 8192 32.7 / 54.0, 32768 57.5 / 133; 32 rows:
+// 8192 tokens 23.9 / 23.8, 32768 47.2 / 43.3; 4 rows: 32768 tokens 45.8 / 26.2.  2 kv heads, 64 rows: 8192
+// tokens 23.4 / 20.5, 32768 29.4 / 30.9; 128 rows: 2048 tokens 17.9 / 17.0, 32768 30.9 / 43.6.
+constexpr int64_t kTensorRows = 64;
+constexpr int64_t kTensorWork = 1 << 20;
 
 // What a call launches, from its sizes alone (the workspace is sized by the same function).
 struct PrefixPlan {
@@ -72,7 +77,7 @@ cudaError_t prefix_plan(int32_t hkv, int32_t hq, int32_t num_seqs, int32_t prefi
 {
     using Fmt = PrefixFormat<true, kD>;
     const int64_t rows = static_cast<int64_t>(num_seqs) * (hq / hkv);
-    pl.tensor = kD == 128 && prefix_len > 0 && rows >= kTensorRows;
+    pl.tensor = kD == 128 && rows >= kTensorRows && hkv * rows * prefix_len >= kTensorWork;
     pl.plan_seqs = num_seqs + (prefix_len > 0 && !pl.tensor ? 1 : 0);
     pl.smem = decode_smem_bytes<Fmt>(pl.plan_seqs, kRowsPerBlock);
     pl.merge_smem = row_merge_smem(pl.plan_seqs);
@@ -83,7 +88,7 @@ cudaError_t prefix_plan(int32_t hkv, int32_t hq, int32_t num_seqs, int32_t prefi
     pl.segments = own + (pl.plan_seqs > num_seqs ? blocks : 0);
     // slots of the plan's pieces (either with or without the prefix), then those of the tensor-core
     // kernel: splits > 1 only while splits * hkv * row_pairs <= SMs, and a pair holds 32 row blocks
-    pl.tc_slots = workspace_bytes_for<Fmt::kTiles>(static_cast<size_t>(pl.ls.sms) * pl.ls.occ * Fmt::kWarps, own);
+    pl.tc_slots = row_slots_bytes<Fmt>(pl.ls, own);
     pl.workspace = pl.tc_slots + (blocks + (kD == 128 ? 32 * static_cast<int64_t>(pl.ls.sms) : 0)) *
                                      slot_floats<Fmt::kTiles>() * sizeof(float);
     if (pl.tensor)
@@ -107,7 +112,12 @@ cudaError_t launch(const DecodeArgs &a, const int32_t *prefix_table, int32_t pre
     p.num_seqs = pl.plan_seqs;
     p.qrows = kRowsPerBlock;
     p.max_segments = pl.segments;
-    p.total_warps = pl.ls.sms * pl.ls.occ * Fmt::kWarps;
+    int64_t cost = max_segments(a.num_kv_heads, a.num_q_heads, a.num_seqs, 0, false) * (a.max_blocks + kKappa);
+    if (pl.plan_seqs > a.num_seqs)
+        cost += a.num_kv_heads * prefix_blocks(a.num_q_heads, a.num_kv_heads, a.num_seqs) *
+                ((static_cast<int64_t>(prefix_len) + kPageSize - 1) / kPageSize + kKappa);
+    const int32_t grid = row_grid<Fmt>(pl.ls, cost);
+    p.total_warps = grid * Fmt::kWarps;
     p.prefix_seq = pl.plan_seqs > a.num_seqs ? a.num_seqs : -1;
     p.prefix_len = prefix_len;
     p.prefix_table = prefix_table;
@@ -116,7 +126,7 @@ cudaError_t launch(const DecodeArgs &a, const int32_t *prefix_table, int32_t pre
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(pl.ls.sms * pl.ls.occ));
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(32 * Fmt::kWarps);
     cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = stream;
@@ -133,12 +143,11 @@ cudaError_t launch(const DecodeArgs &a, const int32_t *prefix_table, int32_t pre
     e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<Fmt, kModePrefix>, *map, p);
     if (e != cudaSuccess)
         return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(max_segments(a.num_kv_heads, a.num_q_heads, a.num_seqs, 0, false),
-                                                               16 * pl.ls.sms)));
-    cfg.blockDim = dim3(32 * kRowWarps);
-    cfg.dynamicSmemBytes = pl.merge_smem;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, row_merge_kernel<kRotate, kD, kModePrefix>, p, pre);
+    const int64_t own = max_segments(a.num_kv_heads, a.num_q_heads, a.num_seqs, 0, false);
+    const int64_t longest = pl.plan_seqs > a.num_seqs
+                                ? a.num_kv_heads * prefix_blocks(a.num_q_heads, a.num_kv_heads, a.num_seqs)
+                                : own;
+    e = launch_row_merge<kRotate, kD, kModePrefix>(p, pre, pl.ls, own, longest, pl.merge_smem, stream);
     if (e != cudaSuccess)
         return e;
     return cudaGetLastError();

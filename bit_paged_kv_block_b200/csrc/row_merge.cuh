@@ -2,6 +2,8 @@
 // decode and the decode with accumulated attention weights).
 #pragma once
 
+#include <algorithm>
+
 #include "int4_format.cuh"
 
 namespace saw {
@@ -14,7 +16,9 @@ struct PrefixPieces {
     int32_t row_blocks, splits;
 };
 
-constexpr int kRowWarps = 4;
+constexpr int kRowWarps = 4;        // warps of a CTA, a row each
+constexpr int kRowWarpsWide = 8;    // warps of a CTA that share one row's pieces
+constexpr int kWidePieces = 16;     // ... from about this many pieces a row on
 
 // One output row's elements of a lane: D / 32 of them, in runs of at most 4 (d = 4 lane + j in each
 // 128-block; for D = 64 d = 2 lane + j).
@@ -39,6 +43,23 @@ struct RowVec {
                 v[b][1] = fmaf(w, x.y, v[b][1]);
             }
         }
+    }
+    __device__ void scale(float f)
+    {
+#pragma unroll
+        for (int b = 0; b < kRuns; b++)
+#pragma unroll
+            for (int j = 0; j < kRun; j++)
+                v[b][j] *= f;
+    }
+    // as fma_row reads it
+    __device__ void store_row(float *row, int lane) const
+    {
+#pragma unroll
+        for (int b = 0; b < kRuns; b++)
+#pragma unroll
+            for (int j = 0; j < kRun; j++)
+                row[128 * b + kRun * lane + j] = v[b][j];
     }
     // the unnormalised Hadamard transform of each block: the run in registers, the rest across lanes
     __device__ void hadamard(int lane)
@@ -83,24 +104,29 @@ struct RowPieces {
     int count, row;
 };
 
-// One CTA per output segment (sequence s, kv head h, block of up to 8 of its heads), one warp per row:
-// the row's pieces (those of its own tokens, then the prefix's) are joined with weights 2^(m_k - M),
-// which the lanes form for 32 pieces at once, so that the loads of the pieces' rows depend on nothing
-// but the list.  Pieces are taken in a fixed order: the result does not depend on timing.  (Folding one
-// piece after another, each waiting for the one before, took 16 us for 17 splits.)
+// One warp per output row, a CTA per segment (sequence s, kv head h, block of up to 8 of its heads): the
+// row's pieces (those of its own tokens, then the prefix's) are joined with weights 2^(m_k - M), which the
+// lanes form for 32 pieces at once, so that the loads of the pieces' rows depend on nothing but the list.
+// Pieces are taken in a fixed order: the result does not depend on timing.  (Folding one piece after
+// another, each waiting for the one before, took 16 us for 17 splits.)  kWide, for few long segments: a CTA
+// per row, whose warps take a share of its pieces each and are joined in warp order (296 pieces of one
+// row: 40 us by one warp).
 // kMode: the shared-prefix decode, which leaves every segment to this kernel; or the decode with
 // accumulated weights (`pre` unused), which finished the segments that were not split and whose rows
 // also get lse = M + log2 l.
-template <bool kRotate, int kD, int kMode>
-__global__ void __launch_bounds__(32 * kRowWarps) row_merge_kernel(const DecodeParams p, const PrefixPieces pre)
+template <bool kRotate, int kD, int kMode, bool kWide>
+__global__ void __launch_bounds__(32 * (kWide ? kRowWarpsWide : kRowWarps))
+    row_merge_kernel(const DecodeParams p, const PrefixPieces pre)
 {
     constexpr bool kPrefix = kMode == kModePrefix;
-    constexpr int kSlot = slot_floats<kD / 16>();
+    constexpr int kSlot = slot_floats<kD / 16>(), kWarps = kWide ? kRowWarpsWide : kRowWarps;
     extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float part_o[kWide ? kWarps : 1][kD];
+    __shared__ float part_m[kWarps], part_l[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int64_t *flags = reinterpret_cast<volatile int64_t *>(smem);
     SeqTables tb;
-    tb.bind(smem + 16 * kRowWarps, p.num_seqs);
+    tb.bind(smem + 16 * kWarps, p.num_seqs);
     scan_sequences<kMode>(p, tb, flags, false);
     Plan plan;
     plan.init(tb, p.num_seqs, p.total_warps, kRowMinSlice);
@@ -112,8 +138,10 @@ __global__ void __launch_bounds__(32 * kRowWarps) row_merge_kernel(const DecodeP
     };
     pdl_wait();
     const int nb = (p.group + kRowsPerBlock - 1) / kRowsPerBlock;
-    for (int o = blockIdx.x; o < p.batch * p.hkv * nb; o += gridDim.x) {
-        const int s = o / (p.hkv * nb), j = o - s * (p.hkv * nb);
+    const int segments = p.batch * p.hkv * nb;
+    for (int64_t o = blockIdx.x; o < (kWide ? static_cast<int64_t>(segments) * kRowsPerBlock : segments); o += gridDim.x) {
+        const int seg = static_cast<int>(kWide ? o / kRowsPerBlock : o);
+        const int s = seg / (p.hkv * nb), j = seg - s * (p.hkv * nb);
         const int h = j / nb, row0 = kRowsPerBlock * (j - h * nb), nrows = min(kRowsPerBlock, p.group - row0);
         const int len = p.seq_lens[s];
         const bool valid = len >= 0 && len <= p.max_blocks * kPageSize;
@@ -122,7 +150,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) row_merge_kernel(const DecodeP
             own = planned(s, j, 0);
         if (!kPrefix && own.count <= 1)
             continue;
-        for (int e = warp; e < nrows; e += kRowWarps) {
+        const int e0 = kWide ? static_cast<int>(o % kRowsPerBlock) : warp;
+        for (int e = e0; e < nrows; e += kWide ? kRowsPerBlock : kWarps) {
             RowPieces part[2] = {own, {nullptr, 0, 0}};
             part[0].row = e;
             const int row = s * p.group + row0 + e;   // the prefix's row of this head
@@ -135,8 +164,11 @@ __global__ void __launch_bounds__(32 * kRowWarps) row_merge_kernel(const DecodeP
             float M = -INFINITY, l = 0.0f;   // l: this lane's share
 #pragma unroll
             for (int q = 0; q < (kPrefix ? 2 : 1); q++) {
-                for (int k0 = 0; k0 < part[q].count; k0 += 32) {
-                    const int n = min(32, part[q].count - k0);
+                // (kWide: this warp's share of the list)
+                const int per = kWide ? (part[q].count + kWarps - 1) / kWarps : part[q].count;
+                const int k1 = kWide ? min(part[q].count, (warp + 1) * per) : per;
+                for (int k0 = kWide ? warp * per : 0; k0 < k1; k0 += 32) {
+                    const int n = min(32, k1 - k0);
                     const float *slot = part[q].base + static_cast<int64_t>(k0) * kSlot;
                     const float mk = lane < n ? slot[static_cast<int64_t>(lane) * kSlot + 8 * kD + part[q].row] : -INFINITY;
                     const float lk = lane < n ? slot[static_cast<int64_t>(lane) * kSlot + 8 * kD + 8 + part[q].row] : 0.0f;
@@ -149,11 +181,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) row_merge_kernel(const DecodeP
                     const float w = mk == -INFINITY ? 0.0f : ex2_approx(mk - top);
                     M = top;
                     l = l * old + lk * w;
-#pragma unroll
-                    for (int b = 0; b < RowVec<kD>::kRuns; b++)
-#pragma unroll
-                        for (int i = 0; i < RowVec<kD>::kRun; i++)
-                            acc.v[b][i] *= old;
+                    acc.scale(old);
                     const float *r = slot + part[q].row * kD;
 #pragma unroll 8
                     for (int k = 0; k < n; k++)
@@ -163,6 +191,28 @@ __global__ void __launch_bounds__(32 * kRowWarps) row_merge_kernel(const DecodeP
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1)
                 l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+            if constexpr (kWide) {
+                acc.store_row(part_o[warp], lane);
+                if (lane == 0) {
+                    part_m[warp] = M;
+                    part_l[warp] = l;
+                }
+                __syncthreads();
+                if (warp == 0) {
+                    for (int w = 0; w < kWarps; w++)
+                        M = fmaxf(M, part_m[w]);
+                    acc = {};
+                    l = 0.0f;
+                    for (int w = 0; w < kWarps; w++) {
+                        const float f = part_m[w] == -INFINITY ? 0.0f : ex2_approx(part_m[w] - M);
+                        l += part_l[w] * f;
+                        acc.fma_row(part_o[w], lane, f);
+                    }
+                }
+                __syncthreads();
+                if (warp > 0)
+                    continue;
+            }
             if (kRotate)
                 acc.hadamard(lane);
             // a row that attended over nothing is zero
@@ -175,7 +225,46 @@ __global__ void __launch_bounds__(32 * kRowWarps) row_merge_kernel(const DecodeP
     }
 }
 
-inline size_t row_merge_smem(int32_t num_seqs) { return 16 * kRowWarps + seq_table_bytes(num_seqs); }
+// CTAs of the decode kernel for at most max_cost pages of work (segments' costs included): no more than
+// there are slices of kRowMinSlice, since a CTA that only finds that out costs its start.
+template <class Fmt>
+inline int32_t row_grid(const LaunchShape &ls, int64_t max_cost)
+{
+    const int64_t slices = max_cost / kRowMinSlice + 1;
+    return static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(ls.sms) * std::min(ls.occ, int(Fmt::kMinBlocks)),
+                                                  (slices + Fmt::kWarps - 1) / Fmt::kWarps));
+}
+
+// Workspace bytes of the pieces' slots: sized for the largest grid, so that a workspace for more
+// sequences covers fewer.
+template <class Fmt>
+inline size_t row_slots_bytes(const LaunchShape &ls, int64_t segments)
+{
+    return workspace_bytes_for<Fmt::kTiles>(static_cast<size_t>(ls.sms) * Fmt::kMinBlocks * Fmt::kWarps, segments);
+}
+
+inline size_t row_merge_smem(int32_t num_seqs) { return 16 * kRowWarpsWide + seq_table_bytes(num_seqs); }
+
+// Queue the row merge of `segments` output segments as a programmatic dependent of the last kernel;
+// `longest`: the segments that share most of the plan's pieces.
+template <bool kRotate, int kD, int kMode>
+cudaError_t launch_row_merge(const DecodeParams &p, const PrefixPieces &pre, const LaunchShape &ls, int64_t segments,
+                             int64_t longest, size_t smem, cudaStream_t stream)
+{
+    const bool wide = p.total_warps > kWidePieces * longest;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(wide ? kRowsPerBlock * segments : segments, 16 * ls.sms)));
+    cfg.blockDim = dim3(32 * (wide ? kRowWarpsWide : kRowWarps));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return wide ? cudaLaunchKernelEx(&cfg, row_merge_kernel<kRotate, kD, kMode, true>, p, pre)
+                : cudaLaunchKernelEx(&cfg, row_merge_kernel<kRotate, kD, kMode, false>, p, pre);
+}
 
 }  // namespace
 }  // namespace saw

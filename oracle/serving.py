@@ -85,14 +85,13 @@ def _f16(bits):
 def rows_fp64(kv_pages, scales, table, n, h, sel) -> np.ndarray:
     """The first n cached vectors (K: sel 0, V: sel 1) of kv head h in the pages of `table`, as
     stored (not rotated back): fp64 [n][D]."""
-    D = 2 * kv_pages.shape[-1]
-    out = np.empty((n, D))
-    for t in range(n):
-        page, off = table[t // PAGE], t % PAGE
-        packed = kv_pages[page, h, sel, off]
-        scale, zero = _f16(scales[page, h, sel, off])
-        out[t, 0::2] = zero + (packed & 15) * scale
-        out[t, 1::2] = zero + (packed >> 4) * scale
+    t = np.arange(n)
+    page, off = np.asarray(table)[t // PAGE], t % PAGE
+    packed = kv_pages[page, h, sel, off]
+    pair = _f16(scales[page, h, sel, off])
+    out = np.empty((n, 2 * kv_pages.shape[-1]))
+    out[:, 0::2] = pair[:, 1:] + (packed & 15) * pair[:, :1]
+    out[:, 1::2] = pair[:, 1:] + (packed >> 4) * pair[:, :1]
     return out
 
 
@@ -123,12 +122,12 @@ def decode_rows_fp64(q_bits, kv_pages, scales, parts, *, sm_scale=None, rotate=T
             w /= w.sum(1, keepdims=True)
             out[s, h * G:(h + 1) * G] = w @ v
             weights[s][h] = w.sum(0)
-            # |q_d| (code scale + |zero|) summed over d, at most: the magnitudes of one logit's terms
+            # |q_d| (15 |scale| + |zero|) summed over d, at most: the magnitudes of one logit's terms
             big = 0.0
-            for t, n in parts[s]:
-                for i in range(n):
-                    scale, zero = _f16(scales[t[i // PAGE], h, 0, i % PAGE])
-                    big = max(big, 15 * abs(scale) + abs(zero))
+            for table, n in parts[s]:
+                t = np.arange(n)
+                pair = np.abs(_f16(scales[np.asarray(table)[t // PAGE], h, 0, t % PAGE]))
+                big = max(big, (15 * pair[:, 0] + pair[:, 1]).max(initial=0.0))
             terms[s, h] = sm_scale * np.abs(qs).sum(1).max() * big
     if rotate:
         out = rotate_f64(out)

@@ -77,7 +77,7 @@ def test_decode_mass_matches_oracle(cuda_device, hq, hkv, d, rotate):
 def test_decode_mass_many_and_few_segments(cuda_device):
     """One long sequence on one kv head (split over every warp), and many short ones."""
     from bit_paged_kv_block_b200 import saw
-    for lens, hq, hkv in (([4000], 2, 1), ([(5 * s) % 37 for s in range(200)], 8, 4)):
+    for lens, hq, hkv in (([4000], 2, 1), ([9001], 6, 1), ([(5 * s) % 37 for s in range(200)], 8, 4)):
         wl, pages, scales, q, mass = _case(lens, hq, hkv, 128, seed=len(lens))
         out, got = _decode(saw, cuda_device, wl, pages, scales, q, mass, lens)
         parts = [[(wl.block_table[s], n)] for s, n in enumerate(lens)]

@@ -158,3 +158,80 @@ def test_prefix_decode_repeats_and_replays(cuda_device, S):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, first)
+
+
+# ---- the prefix on the tensor cores (64 query rows per kv head and 2^20 row-token pairs on) -------
+
+@pytest.mark.parametrize("G,S,prefix", [
+    (16, 64, 1024), (16, 64, 1025), (16, 64, 1087), (16, 64, 1088), (16, 64, 1151), (16, 65, 1152),
+    (4, 18, 14600), (16, 9, 7300), (3, 43, 8192), (1, 100, 10500)])
+def test_prefix_tensor_cores_match_oracle(cuda_device, G, S, prefix):
+    """Row counts of one tile, two, and several pairs, whole and ragged (odd groups, rows past the last
+    block of 8); prefixes that end at, just past and just before the edges of a 128-token block and of
+    its halves; own parts from none on."""
+    from bit_paged_kv_block_b200 import saw
+    lens = [(11 * s) % 50 for s in range(S)]
+    wl, pages, scales, q = _case(prefix, lens, G, 1, 128, seed=prefix + G)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    got = _run(saw, wl, pages, scales, q, prefix, lens, cuda_device, status=status)
+    assert int(status.item()) == 0
+    assert_bf16_close(got, _want(wl, pages, scales, q, prefix, lens), f"G={G} S={S} prefix {prefix}")
+
+
+def test_prefix_tensor_cores_plain_cache_and_heads(cuda_device):
+    from bit_paged_kv_block_b200 import saw
+    lens = [(5 * s) % 30 for s in range(40)]
+    wl, pages, scales, q = _case(2200, lens, 24, 3, 128, seed=3, rotate=False)
+    got = _run(saw, wl, pages, scales, q, 2200, lens, cuda_device, rotate=False)
+    assert_bf16_close(got, _want(wl, pages, scales, q, 2200, lens, rotate=False), "plain, 3 kv heads")
+
+
+def test_prefix_tensor_cores_repeat_flag_and_replay(cuda_device):
+    """The same bits eagerly and replayed; bad lengths zero their rows; a bad prefix page is flagged."""
+    from bit_paged_kv_block_b200 import saw
+    S, prefix = 64, 1100
+    lens = [(13 * s) % 90 for s in range(S)]
+    wl, pages, scales, q = _case(prefix, lens, 16, 1, 128, seed=34)
+    want = _want(wl, pages, scales, q, prefix, lens)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    bad = list(lens)
+    bad[1], bad[2] = -3, 16 * wl.block_table.shape[1] + 1
+    got = _run(saw, wl, pages, scales, q, prefix, bad, cuda_device, status=status)
+    assert int(status.item()) == saw.SAW_DEV_BAD_SEQ_LEN
+    zeroed = want.copy()
+    zeroed[1:3] = 0.0
+    assert_bf16_close(got, zeroed, "bad lengths")
+    status.zero_()
+    broken = synth.Workload(**{**wl.__dict__})
+    broken.block_table = wl.block_table.copy()
+    broken.block_table[0, 3] = pages.shape[0]
+    _run(saw, broken, pages, scales, q, prefix, lens, cuda_device, status=status)
+    assert int(status.item()) == saw.SAW_DEV_BAD_PAGE
+    kv, sc = device_cache_from(pages, scales, cuda_device)
+    table = torch.from_numpy(wl.block_table).to(cuda_device)
+    args = (q.to(cuda_device), kv, sc, table[0].contiguous(), prefix, table[1:].contiguous(),
+            torch.tensor(lens, dtype=torch.int32, device=cuda_device))
+    ws = saw.allocate_prefix_workspace(1, 16, S, prefix, cuda_device)
+    first, out = (torch.empty(S, 16, 128, dtype=torch.bfloat16, device=cuda_device) for _ in range(2))
+    saw.saw_paged_decode_attn_prefix(*args, first, ws)
+    torch.cuda.synchronize()
+    assert_bf16_close(first, want, "eager")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        saw.saw_paged_decode_attn_prefix(*args, out, ws)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        ws.fill_(0xFF)                     # NaN bits: nothing of the last call is read
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+
+
+def test_prefix_few_rows_many_pieces(cuda_device):
+    """One sequence behind a long prefix: each row joined from hundreds of pieces by a CTA of its own;
+    also at D = 64 and 256, and the decode with weights over one long sequence."""
+    from bit_paged_kv_block_b200 import saw
+    for hq, hkv, d, prefix in ((4, 1, 128, 9000), (16, 1, 64, 5000), (6, 2, 256, 4001)):
+        wl, pages, scales, q = _case(prefix, [9], hq, hkv, d, seed=d)
+        got = _run(saw, wl, pages, scales, q, prefix, [9], cuda_device)
+        assert_bf16_close(got, _want(wl, pages, scales, q, prefix, [9]), f"{hq}/{hkv}/{d}")
