@@ -115,13 +115,21 @@ __global__ void __launch_bounds__(kMassThreads) mass_accumulate_kernel(const Mas
     }
 }
 
+cudaError_t raise_accumulate_smem(size_t bytes)
+{
+    static SmemCache cache;
+    static const void *const kernels[] = {reinterpret_cast<const void *>(mass_accumulate_kernel<1>),
+                                          reinterpret_cast<const void *>(mass_accumulate_kernel<2>)};
+    return raise_smem(cache, kernels, 2, bytes);
+}
+
 // The page format for G query heads per kv head: the query's low parts in spare MMA columns up to 4.
 template <bool kRotate, int kD, bool kFew>
 using MassFormat = Int4Format<kRotate, kD, kFew ? kRoleMass4 : kRoleMass>;
 constexpr int kFewHeads = 4;
 
 template <int kD, bool kFew>
-cudaError_t mass_shape(size_t smem, size_t merge_smem, LaunchShape &out)
+cudaError_t mass_shape(size_t smem, LaunchShape &out)
 {
     static ShapeCache shapes;
     static const void *const decode_kernels[kShapeVariants] = {
@@ -129,13 +137,8 @@ cudaError_t mass_shape(size_t smem, size_t merge_smem, LaunchShape &out)
         reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<false, kD, kFew>, kModeDecode>),
         reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<true, kD, kFew>, kModeDecode>),
         reinterpret_cast<const void *>(paged_decode_kernel<MassFormat<false, kD, kFew>, kModeDecode>)};
-    static const void *const merge_kernels[kShapeVariants] = {
-        reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModeDecode, false>),
-        reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModeDecode, false>),
-        reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModeDecode, true>),
-        reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModeDecode, true>)};
-    return decode::launch_shape(shapes, decode_kernels, merge_kernels, 32 * MassFormat<true, kD, kFew>::kWarps,
-                                smem, merge_smem, out);
+    return decode::launch_shape(shapes, decode_kernels, decode_kernels, 32 * MassFormat<true, kD, kFew>::kWarps,
+                                smem, 0, out);   // 0: the kernels that follow raise their own
 }
 
 // Workspace: the split-K slots, lse [S][Hq], then the logits of every page the block table can hold.
@@ -150,8 +153,11 @@ cudaError_t mass_workspace(int32_t hkv, int32_t hq, int32_t num_seqs, int32_t ma
     using Fmt = MassFormat<true, kD, false>;   // the layout is the same for all variants
     const int32_t qrows = query_rows(hkv, hq, false);
     const size_t smem = decode_smem_bytes<Fmt>(num_seqs, qrows);
-    const cudaError_t e = hq / hkv <= kFewHeads ? mass_shape<kD, true>(smem, row_merge_smem(num_seqs), ls)
-                                                : mass_shape<kD, false>(smem, row_merge_smem(num_seqs), ls);
+    cudaError_t e = hq / hkv <= kFewHeads ? mass_shape<kD, true>(smem, ls) : mass_shape<kD, false>(smem, ls);
+    if (e == cudaSuccess)
+        e = raise_row_merge_smem<kD, kModeDecode>(row_merge_smem(num_seqs));
+    if (e == cudaSuccess)
+        e = raise_accumulate_smem(mass_smem_bytes(num_seqs));
     if (e != cudaSuccess)
         return e;
     const int64_t segments = max_segments(hkv, hq, num_seqs, 0, false);

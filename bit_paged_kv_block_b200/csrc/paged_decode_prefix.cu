@@ -43,13 +43,9 @@ cudaError_t prefix_shape(size_t smem, size_t merge_smem, LaunchShape &out)
         reinterpret_cast<const void *>(paged_decode_kernel<PrefixFormat<false, kD>, kModePrefix>),
         reinterpret_cast<const void *>(paged_decode_kernel<PrefixFormat<true, kD>, kModePrefix>),
         reinterpret_cast<const void *>(paged_decode_kernel<PrefixFormat<false, kD>, kModePrefix>)};
-    static const void *const merge_kernels[kShapeVariants] = {
-        reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModePrefix, false>),
-        reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModePrefix, false>),
-        reinterpret_cast<const void *>(row_merge_kernel<true, kD, kModePrefix, true>),
-        reinterpret_cast<const void *>(row_merge_kernel<false, kD, kModePrefix, true>)};
-    return decode::launch_shape(shapes, decode_kernels, merge_kernels, 32 * PrefixFormat<true, kD>::kWarps,
-                                smem, merge_smem, out);
+    const cudaError_t e = decode::launch_shape(shapes, decode_kernels, decode_kernels,
+                                               32 * PrefixFormat<true, kD>::kWarps, smem, 0, out);
+    return e == cudaSuccess ? raise_row_merge_smem<kD, kModePrefix>(merge_smem) : e;
 }
 
 // The prefix goes to the tensor cores from 64 query rows per kv head and 2^20 (kv head, row, token) triples

@@ -86,6 +86,22 @@ def test_decode_mass_many_and_few_segments(cuda_device):
         _assert_mass(got, mass, wl, lens, weights, terms, 128)
 
 
+def test_decode_mass_batches_and_groups_in_turn(cuda_device):
+    """Many sequences (tables past 48 KB of shared memory), then few with the other group size, then many
+    again: what a call may use does not depend on the calls before it."""
+    from bit_paged_kv_block_b200 import saw
+    cases = []
+    for S, hq in ((2600, 2), (3, 8), (2600, 2), (2500, 8), (200, 2), (2500, 8)):
+        lens = [(7 * s) % 19 % 4 for s in range(S)]
+        wl, pages, scales, q, mass = _case(lens, hq, 1, 128, seed=hq)
+        cases.append((wl, q, mass, lens, pages, scales, *_decode(saw, cuda_device, wl, pages, scales, q, mass, lens)))
+    for wl, q, mass, lens, pages, scales, out, got in cases:
+        parts = [[(wl.block_table[s], n)] for s, n in enumerate(lens)]
+        want, weights, terms = serving.decode_rows_fp64(u16(q), pages, scales, parts)
+        assert_bf16_close(out, want, f"{len(lens)} sequences")
+        _assert_mass(got, mass, wl, lens, weights, terms, 128)
+
+
 def test_decode_mass_shared_pages_and_flags(cuda_device):
     """Two sequences over the same pages both add; bad lengths and page ids are flagged, add nothing,
     and leave the others right."""

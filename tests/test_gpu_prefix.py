@@ -235,3 +235,14 @@ def test_prefix_few_rows_many_pieces(cuda_device):
         wl, pages, scales, q = _case(prefix, [9], hq, hkv, d, seed=d)
         got = _run(saw, wl, pages, scales, q, prefix, [9], cuda_device)
         assert_bf16_close(got, _want(wl, pages, scales, q, prefix, [9]), f"{hq}/{hkv}/{d}")
+
+
+def test_prefix_batches_in_turn(cuda_device):
+    """Tables past 48 KB of shared memory, with the prefix in the plan and on the tensor cores, and small
+    calls between."""
+    from bit_paged_kv_block_b200 import saw
+    for S, hq, prefix in ((2600, 2, 40), (3, 2, 40), (2600, 2, 300), (2, 4, 33), (2600, 2, 40)):
+        lens = [(7 * s) % 19 % 4 for s in range(S)]
+        wl, pages, scales, q = _case(prefix, lens, hq, 1, 128, seed=S)
+        got = _run(saw, wl, pages, scales, q, prefix, lens, cuda_device)
+        assert_bf16_close(got, _want(wl, pages, scales, q, prefix, lens), f"{S} sequences")
