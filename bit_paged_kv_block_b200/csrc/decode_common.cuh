@@ -752,6 +752,8 @@ __global__ void __launch_bounds__(32 * Fmt::kWarps, Fmt::kMinBlocks)
         F1 = F0 + tb.npg[s];
     } else {
         if (plan.P == 0 || u >= plan.W) {
+            if (plan.P == 0)
+                pdl_wait();   // no CTA has work: not over before the kernel this one depends on
             pdl_exit();
             return;
         }

@@ -165,6 +165,8 @@ cudaError_t mass_workspace(int32_t hkv, int32_t hq, int32_t num_seqs, int32_t ma
     w.lse = round(hq / hkv <= kFewHeads ? row_slots_bytes<MassFormat<true, kD, true>>(ls, segments)
                                         : row_slots_bytes<Fmt>(ls, segments));
     w.logits = w.lse + round(static_cast<size_t>(num_seqs) * hq * sizeof(float));
+    if (segments > (int64_t(1) << 52) / (static_cast<int64_t>(max_blocks) * kPageSize * qrows))
+        return cudaErrorInvalidValue;   // more than any memory
     w.total = w.logits + static_cast<size_t>(segments) * max_blocks * kPageSize * qrows * sizeof(float);
     return cudaSuccess;
 }

@@ -15,9 +15,10 @@
 // Tensor memory (512 columns): O of the two tiles, then S / P of the two tiles.
 //
 // The running maximum moves only when a row exceeds it by kLag (log2 units): moving it rescales O in
-// tensor memory.  Weights enter as 2^(s - m + kLift) with kLag + kLift = 15, within fp16's range, and
-// flush to 0 only below 2^(-14 - kLift) of the reference (these tensor cores flush subnormals).  The
-// lift cancels: O and l carry it alike, and the piece's maximum is stored less it.
+// tensor memory (64 sequences behind 32768 tokens at 64 heads: 109 us with a lag of 6, 111 with 4, 114
+// with 1).  Weights enter as 2^(s - m + kLift) with 2^(kLag + kLift) = 61147, within fp16's range, and
+// flush to 0 only below 2^(-14 - kLift) = 2^-23.9 of the reference (these tensor cores flush subnormals).
+// The lift cancels: O and l carry it alike, and the piece's maximum is stored less it.
 // Dequantizing in the producers keeps every per-token factor out of the softmax (prefill_tc.cu applies
 // scales and zero points to the logits and weights instead: twice the instructions per element); the
 // price is one rounding of each cached value to fp16 (2^-11 relative at most, as for the query).
@@ -39,9 +40,8 @@ constexpr int kRows = 128;                   // M: rows of a tile
 constexpr int kTok = 128;                    // tokens of a block
 constexpr int kHalfTile = kTok * 128;        // bytes of one 64-wide half (128 B rows) of a tile
 constexpr float kHadC = 0.0883883461356163f;
-constexpr float kQLift = 16.0f;              // query entries enter scaled by 2^4, clear of subnormals
 constexpr float kLag = 6.0f;                 // log2: how far a row may exceed its reference maximum
-constexpr float kLift = 9.0f;
+constexpr float kLift = 9.9f;
 
 // shared memory (from a 1024-byte aligned base)
 constexpr int kPtQ = 0;                               // 2 tiles x 2 halves x [128 rows][128 B]
@@ -432,14 +432,28 @@ __global__ void __launch_bounds__(kPtThreads, 1) prefix_tc_kernel(const PrefixTc
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t so = s_col(t) + lanes, oo = o_col(t) + lanes;
         const int r = row0 + tid;
-        float m_ref = -INFINITY;
+        float m_ref = -INFINITY, unlift = 1.0f;
         uint64_t l2 = f2_pack(0.0f, 0.0f);
         bool ok = __all_sync(0xFFFFFFFFu, tc_wait(s_full(t), 0, abort_flag));
         if (ok) {
             // the rotated query, scaled, as fp16 over the raw one
             tc_fence_after();
             const uint32_t tile = sbase + kPtQ + t * 2 * kHalfTile;
-            const float mul = p.q_mult * kQLift;
+            float amax = 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < 4; c++) {
+                uint32_t a[32];
+                tmem_ld32_async(so + 32 * c, a);
+                tmem_wait(a);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2)
+                    amax = fmax3(amax, fabsf(__uint_as_float(a[i])), fabsf(__uint_as_float(a[i + 1])));
+            }
+            // by a power of two of the row's own: its largest entry at 2^12, so that neither a large query
+            // (or sm_scale) passes fp16's range nor a small one falls among its subnormals
+            const uint32_t ex = min(max((__float_as_uint(amax * fabsf(p.q_mult)) >> 23) & 255u, 64u), 190u);
+            const float mul = p.q_mult * __uint_as_float((266u - ex) << 23);
+            unlift = __uint_as_float((ex - 12u) << 23);
 #pragma unroll 1
             for (int c = 0; c < 4; c++) {
                 uint32_t a[32];
@@ -458,7 +472,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prefix_tc_kernel(const PrefixTc
             tc_fence_before();
             tc_arrive(p_full(t));
         }
-        const uint64_t unlift = f2_pack(1.0f / kQLift, 1.0f / kQLift);
+        const uint64_t un2 = f2_pack(unlift, unlift);
         for (int kb = 0; ok && kb < nb; kb++) {
             ok = tc_wait(s_full(t), static_cast<uint32_t>(kb + 1) & 1u, abort_flag);
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -486,7 +500,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prefix_tc_kernel(const PrefixTc
                 }
                 mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
             }
-            mx *= 1.0f / kQLift;
+            mx *= unlift;
             const bool grow = mx > m_ref + kLag;
             if (__any_sync(0xFFFFFFFFu, grow)) {
                 const float alpha = grow ? ex2_approx(m_ref - mx) : 1.0f;   // 0 on the first block
@@ -519,7 +533,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prefix_tc_kernel(const PrefixTc
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
                     float y0, y1;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), unlift, sh2), y0, y1);
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), un2, sh2), y0, y1);
                     const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
                     l2 = f2_add(l2, f2_pack(e0, e1));
                     x[i >> 1] = half2_as_u32(__floats2half2_rn(e0, e1));

@@ -1015,7 +1015,7 @@ static bool decode_sizes_ok(const saw_cache_desc *cache, int32_t num_q_heads, in
 size_t saw_paged_decode_prefix_workspace_bytes(const saw_cache_desc *cache, int32_t num_q_heads,
                                                int32_t num_seqs, int32_t prefix_len)
 {
-    if (!decode_sizes_ok(cache, num_q_heads, num_seqs) || prefix_len < 0)
+    if (!decode_sizes_ok(cache, num_q_heads, num_seqs) || prefix_len < 0 || prefix_len > (1 << 30))
         return 0;
     return saw::decode_prefix_workspace_bytes(cache->num_kv_heads, num_q_heads, num_seqs, prefix_len,
                                               cache->head_dim);
@@ -1032,7 +1032,7 @@ static int decode_prefix_impl(const saw_cache_desc *cache, int32_t num_q_heads, 
                                    seq_lens, num_seqs, sm_scale, out);
     if (rc != SAW_OK)
         return rc;
-    if (prefix_len < 0 || prefix_len > INT32_MAX - 16)
+    if (prefix_len < 0 || prefix_len > (1 << 30))
         return SAW_ERR_INVALID_ARGUMENT;
     if (num_seqs == 0)
         return SAW_OK;
@@ -1169,12 +1169,14 @@ int saw_evict_paged(const saw_cache_desc *cache, uint8_t *kv_pages, void *scales
         return rc;
     if (num_seqs < 0 || keep < 1 || sink < 0 || recent < 0 || int64_t(sink) + recent > keep)
         return SAW_ERR_INVALID_ARGUMENT;
+    if (keep > (1 << 30))
+        return SAW_ERR_UNSUPPORTED;
     if (num_seqs == 0)
         return SAW_OK;
     if (!kv_pages || !scales || !mass || !block_table || !seq_lens || !new_table || !new_lens || !kept ||
         max_blocks_per_seq <= 0 || new_blocks <= 0 || cache->num_pages == 0 ||
-        int64_t(max_blocks_per_seq) * 16 > INT32_MAX || int64_t(new_blocks) * 16 > INT32_MAX)
-        return SAW_ERR_INVALID_ARGUMENT;
+        int64_t(max_blocks_per_seq) * 16 > (1 << 30) || int64_t(new_blocks) * 16 > INT32_MAX)
+        return SAW_ERR_INVALID_ARGUMENT;   // (token indices, rounded up to whole pages, in 32 bits)
     if (!aligned(kv_pages, 16) || !aligned(scales, 16) || !aligned(mass, 16) || !aligned(block_table, 4) ||
         !aligned(seq_lens, 4) || !aligned(new_table, 4) || !aligned(new_lens, 4) || !aligned(kept, 4))
         return SAW_ERR_INVALID_ARGUMENT;

@@ -447,9 +447,13 @@ int saw_rope_quantize_paged_plain(const saw_cache_desc *cache, const saw_rope *r
  * alone; with prefix_len = 0 (prefix_table may be NULL) the call is a plain decode; a row that attends
  * over nothing is zero, and so are the rows of a sequence whose length is out of range
  * (SAW_DEV_BAD_SEQ_LEN).
- * out: bf16 [S][Hq][D], rounded once at the end.  Arithmetic as saw_paged_decode_attn.  workspace: at
- * least saw_paged_decode_prefix_workspace_bytes() for these sizes (a larger num_seqs or prefix_len
- * covers a smaller one at the same heads), 256-byte aligned, no initialisation needed. */
+ * out: bf16 [S][Hq][D], rounded once at the end.  Arithmetic as saw_paged_decode_attn, except that a
+ * prefix with enough query rows (head_dim 128, from 64 rows a kv head on) enters the tensor cores as
+ * fp16 values: a cached value is rounded to fp16 once more, below 2^-14 it counts as 0 and beyond 65504
+ * it is infinite, and a weight below 2^-23 of its row's largest counts as 0.
+ * workspace: at least saw_paged_decode_prefix_workspace_bytes() for these sizes (a larger num_seqs or
+ * prefix_len covers a smaller one at the same heads), 256-byte aligned, no initialisation needed.
+ * 0 <= prefix_len <= 2^30. */
 size_t saw_paged_decode_prefix_workspace_bytes(const saw_cache_desc *cache, int32_t num_q_heads,
                                                int32_t num_seqs, int32_t prefix_len);
 int saw_paged_decode_attn_prefix(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
@@ -507,8 +511,9 @@ int saw_paged_decode_attn_mass_plain(const saw_cache_desc *cache, int32_t num_q_
  * The old pages are only read, so they may be shared between sequences; the new ones must not be
  * among them, nor appear twice, and new_lens must not be seq_lens.  A length out of range, or
  * n > 16 * new_blocks, leaves the sequence out (SAW_DEV_BAD_SEQ_LEN, new_lens[s] = 0); a page id
- * out of range skips its tokens (SAW_DEV_BAD_PAGE).  0 <= sink, 0 <= recent, 1 <= keep,
- * sink + recent <= keep.  The cache may be a rotated or a plain INT4 one. */
+ * out of range skips its tokens (SAW_DEV_BAD_PAGE).  0 <= sink, 0 <= recent, 1 <= keep <= 2^30,
+ * sink + recent <= keep, 16 * max_blocks_per_seq <= 2^30.  The cache may be a rotated or a plain INT4
+ * one. */
 int saw_evict_paged(const saw_cache_desc *cache, uint8_t *kv_pages, void *scales, float *mass,
                     const int32_t *block_table, int32_t max_blocks_per_seq, const int32_t *seq_lens,
                     int32_t num_seqs, const int32_t *new_table, int32_t new_blocks,

@@ -125,6 +125,7 @@ def test_bf16_decode_checks(call):
 def test_prefix_and_mass_checks():
     assert _prefix(prefix=-1) == INVALID
     assert _prefix(prefix=2 ** 31 - 1) == INVALID
+    assert _prefix(prefix=2 ** 30 + 1) == INVALID
     assert _prefix(table=0) == INVALID
     assert _prefix(table=2) == INVALID
     assert _mass(mass=0) == INVALID
@@ -134,6 +135,7 @@ def test_prefix_and_mass_checks():
     for call in (lambda hq, s: f(ctypes.byref(d), hq, s, 100), lambda hq, s: g(ctypes.byref(d), hq, s, 4)):
         assert call(12, 4) == 0 and call(136, 4) == 0 and call(32, -1) == 0
     assert f(ctypes.byref(d), 32, 4, -1) == 0
+    assert f(ctypes.byref(d), 32, 4, 2 ** 30 + 1) == 0
     assert g(ctypes.byref(d), 32, 4, 0) == 0
 
 
@@ -161,6 +163,8 @@ def test_evict_checks():
     assert _evict(new_lens=16) == INVALID                              # new_lens is seq_lens
     assert _evict(kept=2) == INVALID
     assert _evict(S=2 ** 30) == UNSUPPORTED
+    assert _evict(keep=2 ** 30 + 1) == UNSUPPORTED
+    assert _evict(max_blocks=2 ** 26 + 1) == INVALID                   # past 2^30 tokens
     assert _evict(S=0, pages=0) == OK
 
 

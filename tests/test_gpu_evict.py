@@ -394,3 +394,43 @@ def test_step_rope_matches_append_then_decode(cuda_device):
     torch.cuda.synchronize()
     assert torch.equal(q_rot.view(torch.int16), q_rot2.view(torch.int16))
     assert torch.equal(kv, kv2) and torch.equal(out, out2)
+
+
+@pytest.mark.parametrize("with_mass", [False, True])
+def test_step_rope_appends_behind_empty_lengths(cuda_device, with_mass):
+    """Lengths of zero: nothing to decode, but the step is over only once the tokens are in the cache."""
+    from bit_paged_kv_block_b200 import saw
+    dev = cuda_device
+    S = 300
+    kv = torch.zeros(S, 2, 2, 16, 64, dtype=torch.uint8, device=dev)
+    sc = torch.zeros(S, 2, 2, 16, 2, dtype=torch.float16, device=dev)
+    kv2, sc2 = kv.clone(), sc.clone()
+    table = torch.zeros(64, 128, device=dev)
+    saw.saw_rope_table(table, saw.rope_scaling())
+    g = torch.Generator().manual_seed(2)
+    q = torch.randn(S, 8, 128, generator=g).to(torch.bfloat16).to(dev)
+    k, v = (torch.randn(S, 2, 128, generator=g).to(torch.bfloat16).to(dev) for _ in range(2))
+    pos = torch.arange(S, device=dev) % 64
+    slots = torch.arange(S, device=dev) * 16 + 3
+    bt = torch.arange(S, dtype=torch.int32, device=dev).view(S, 1)
+    lens = torch.zeros(S, dtype=torch.int32, device=dev)
+    q_rot = torch.empty_like(q)
+    if with_mass:
+        mass = torch.ones(S, 2, 16, device=dev)
+        out = torch.full((S, 8, 128), float("nan"), dtype=torch.bfloat16, device=dev)
+        ws = saw.allocate_mass_workspace(2, 8, S, 1, dev)
+        saw.saw_decode_step_rope(q, k, v, pos, slots, (table, False), q_rot, kv, sc, bt, lens, out, ws, mass=mass)
+    else:
+        out = torch.full((S, 8, 128), float("nan"), device=dev)
+        ws = saw.allocate_workspace(2, 8, S, dev)
+        saw.saw_decode_step_rope(q, k, v, pos, slots, (table, False), q_rot, kv, sc, bt, lens, out, ws)
+    got, got_q = kv.clone(), q_rot.clone()          # queued right behind the step
+    q_rot2 = torch.empty_like(q)
+    saw.saw_rope_rotate_quantize_paged(q, k, v, pos, slots, (table, False), q_rot2, kv2, sc2)
+    torch.cuda.synchronize()
+    assert torch.equal(got, kv2) and torch.equal(got_q, q_rot2)
+    assert bool((out == 0).all())
+    if with_mass:
+        want = torch.ones(S, 2, 16)
+        want[:, :, 3] = 0.0
+        assert torch.equal(mass.cpu(), want)

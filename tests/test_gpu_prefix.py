@@ -246,3 +246,23 @@ def test_prefix_batches_in_turn(cuda_device):
         wl, pages, scales, q = _case(prefix, lens, hq, 1, 128, seed=S)
         got = _run(saw, wl, pages, scales, q, prefix, lens, cuda_device)
         assert_bf16_close(got, _want(wl, pages, scales, q, prefix, lens), f"{S} sequences")
+
+
+@pytest.mark.parametrize("big", [2.0 ** 20, 2.0 ** -12])
+def test_prefix_tensor_cores_query_magnitudes(cuda_device, big):
+    """Queries far outside fp16's range once scaled: one element, on a channel whose largest key leads the
+    next by 2% of it or more (logits are off by 2^-10 of themselves at most), so that a huge query takes
+    that token's value; a tiny one the mean."""
+    from bit_paged_kv_block_b200 import saw
+    S, prefix, hq = 64, 1100, 16
+    wl, pages, scales, q = _case(prefix, [0] * S, hq, 1, 128, seed=81, rotate=False)
+    K = serving.rows_fp64(pages, scales, wl.block_table[0], prefix, 0, 0)
+    top = np.sort(K, axis=0)
+    clear = [c for c in range(128) if top[-1, c] - top[-2, c] >= 0.02 * top[-1, c] > 0.02]
+    assert len(clear) >= 4
+    q.zero_()
+    for s in range(S):
+        for h in range(hq):
+            q[s, h, clear[(s + h) % len(clear)]] = big
+    got = _run(saw, wl, pages, scales, q, prefix, [0] * S, cuda_device, rotate=False)
+    assert_bf16_close(got, _want(wl, pages, scales, q, prefix, [0] * S, rotate=False), f"{big}")
