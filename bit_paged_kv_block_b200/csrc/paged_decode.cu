@@ -27,7 +27,7 @@
 //   * O^T[128 d x 8 heads] += V_codes^T . P'^T with P' = p * scale_V in fp16 and the zero
 //     point added in fp32 through sum_t p_t zero_t.
 // The work split, the piece loop, the split-K slots and the merge kernel are generic over the
-// page format and live in decode_common.cuh; this file is the INT4 page format (Int4Format).
+// page format and live in decode_common.cuh; the INT4 page format (Int4Format) is int4_format.cuh.
 // The query of the next segment is bulk-copied into a per-warp buffer while the current one is
 // processed.  The query dimension d of QK and the value dimension of PV are consumed in a
 // permuted order (both sides permuted alike), which lets every thread unpack whole 32-bit code
