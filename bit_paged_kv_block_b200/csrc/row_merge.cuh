@@ -28,22 +28,26 @@ struct RowVec {
     static constexpr int kRuns = kD == 256 ? 2 : 1, kRun = kD == 64 ? 2 : 4;
     float v[kRuns][kRun];
 
-    __device__ void fma_row(const float *row, int lane, float w)
+    __device__ void load_row(const float *row, int lane)
     {
 #pragma unroll
         for (int b = 0; b < kRuns; b++) {
             if constexpr (kRun == 4) {
                 const float4 x = *reinterpret_cast<const float4 *>(row + 128 * b + 4 * lane);
-                v[b][0] = fmaf(w, x.x, v[b][0]);
-                v[b][1] = fmaf(w, x.y, v[b][1]);
-                v[b][2] = fmaf(w, x.z, v[b][2]);
-                v[b][3] = fmaf(w, x.w, v[b][3]);
+                v[b][0] = x.x, v[b][1] = x.y, v[b][2] = x.z, v[b][3] = x.w;
             } else {
                 const float2 x = *reinterpret_cast<const float2 *>(row + 2 * lane);
-                v[b][0] = fmaf(w, x.x, v[b][0]);
-                v[b][1] = fmaf(w, x.y, v[b][1]);
+                v[b][0] = x.x, v[b][1] = x.y;
             }
         }
+    }
+    __device__ void fma(const RowVec &x, float w)
+    {
+#pragma unroll
+        for (int b = 0; b < kRuns; b++)
+#pragma unroll
+            for (int j = 0; j < kRun; j++)
+                v[b][j] = fmaf(w, x.v[b][j], v[b][j]);
     }
     __device__ void scale(float f)
     {
@@ -53,7 +57,7 @@ struct RowVec {
             for (int j = 0; j < kRun; j++)
                 v[b][j] *= f;
     }
-    // as fma_row reads it
+    // as load_row reads it
     __device__ void store_row(float *row, int lane) const
     {
 #pragma unroll
@@ -107,11 +111,12 @@ struct RowPieces {
 
 // One warp per output row, a CTA per segment (sequence s, kv head h, block of up to 8 of its heads): the
 // row's pieces (those of its own tokens, then the prefix's) are joined with weights 2^(m_k - M), which the
-// lanes form for 32 pieces at once, so that the loads of the pieces' rows depend on nothing but the list.
-// Pieces are taken in a fixed order: the result does not depend on timing.  (Folding one piece after
-// another, each waiting for the one before, took 16 us for 17 splits.)  kWide, for few long segments: a CTA
-// per row, whose warps take a share of its pieces each and are joined in warp order (296 pieces of one
-// row: 40 us by one warp).
+// lanes form for 32 pieces at once, while the first 16 pieces' rows are on their way: loads depend on
+// nothing but the list.  Bound by their latency.  Pieces are taken in a fixed order: the result does not
+// depend on timing.  (64 sequences behind 8192 tokens: 54 us in all, with rows loaded after their weights
+// 58; 4 behind 259: 12.2 and 13.6.  Folding one piece after another, each waiting for the one before, took
+// 16 us for 17 splits.)  kWide, for few long segments: a CTA per row, whose warps take a share of its
+// pieces each and are joined in warp order (296 pieces of one row: 40 us by one warp).
 // kMode: the shared-prefix decode, which leaves every segment to this kernel; or the decode with
 // accumulated weights (`pre` unused), which finished the segments that were not split and whose rows
 // also get lse = M + log2 l.
@@ -120,6 +125,7 @@ __global__ void __launch_bounds__(32 * (kWide ? kRowWarpsWide : kRowWarps))
     row_merge_kernel(const DecodeParams p, const PrefixPieces pre)
 {
     constexpr bool kPrefix = kMode == kModePrefix;
+    constexpr int kChunk = kD == 256 ? 8 : 16;   // rows of pieces in flight: 64 registers at most
     constexpr int kSlot = slot_floats<kD / 16>(), kWarps = kWide ? kRowWarpsWide : kRowWarps;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float part_o[kWide ? kWarps : 1][kD];
@@ -153,40 +159,58 @@ __global__ void __launch_bounds__(32 * (kWide ? kRowWarpsWide : kRowWarps))
             continue;
         const int e0 = kWide ? static_cast<int>(o % kRowsPerBlock) : warp;
         for (int e = e0; e < nrows; e += kWide ? kRowsPerBlock : kWarps) {
-            RowPieces part[2] = {own, {nullptr, 0, 0}};
-            part[0].row = e;
+            // one list: the pieces of the row's own tokens, then the prefix's
+            RowPieces first = own, then = {nullptr, 0, 0};
+            first.row = e;
             const int row = s * p.group + row0 + e;   // the prefix's row of this head
             if (kPrefix && valid && pre.splits > 0)
-                part[1] = {pre.slots + (static_cast<int64_t>(h) * pre.row_blocks + row / kRowsPerBlock) * pre.splits * kSlot,
-                           pre.splits, row % kRowsPerBlock};
+                then = {pre.slots + (static_cast<int64_t>(h) * pre.row_blocks + row / kRowsPerBlock) * pre.splits * kSlot,
+                        pre.splits, row % kRowsPerBlock};
             else if (kPrefix && valid && p.prefix_seq >= 0)
-                part[1] = planned(p.prefix_seq, h * tb.nbk[p.prefix_seq] + row / kRowsPerBlock, row % kRowsPerBlock);
+                then = planned(p.prefix_seq, h * tb.nbk[p.prefix_seq] + row / kRowsPerBlock, row % kRowsPerBlock);
+            auto slot_of = [&](int k, int per_row) {   // its slot, at its row of per_row values
+                const bool a = !kPrefix || k < first.count;
+                return (a ? first.base : then.base) + static_cast<int64_t>(a ? k : k - first.count) * kSlot +
+                       (a ? first.row : then.row) * per_row;
+            };
             RowVec<kD> acc = {};
             float M = -INFINITY, l = 0.0f;   // l: this lane's share
+            // (kWide: this warp's share of the list)
+            const int total = first.count + then.count, per = kWide ? (total + kWarps - 1) / kWarps : total;
+            const int k1 = kWide ? min(total, (warp + 1) * per) : total;
+            for (int k0 = kWide ? warp * per : 0; k0 < k1; k0 += 32) {
+                const int n = min(32, k1 - k0);
+                const float *head = slot_of(min(k0 + lane, k1 - 1), 1) + 8 * kD;
+                const float mk = lane < n ? head[0] : -INFINITY, lk = lane < n ? head[8] : 0.0f;
+                // the first rows are on their way while the weights are formed
+                RowVec<kD> x[kChunk];
 #pragma unroll
-            for (int q = 0; q < (kPrefix ? 2 : 1); q++) {
-                // (kWide: this warp's share of the list)
-                const int per = kWide ? (part[q].count + kWarps - 1) / kWarps : part[q].count;
-                const int k1 = kWide ? min(part[q].count, (warp + 1) * per) : per;
-                for (int k0 = kWide ? warp * per : 0; k0 < k1; k0 += 32) {
-                    const int n = min(32, k1 - k0);
-                    const float *slot = part[q].base + static_cast<int64_t>(k0) * kSlot;
-                    const float mk = lane < n ? slot[static_cast<int64_t>(lane) * kSlot + 8 * kD + part[q].row] : -INFINITY;
-                    const float lk = lane < n ? slot[static_cast<int64_t>(lane) * kSlot + 8 * kD + 8 + part[q].row] : 0.0f;
-                    float top = mk;
+                for (int k = 0; k < kChunk; k++)
+                    if (k < n)
+                        x[k].load_row(slot_of(k0 + k, kD), lane);
+                float top = mk;
 #pragma unroll
-                    for (int d = 1; d < 32; d <<= 1)
-                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                    top = fmaxf(top, M);
-                    const float old = M == -INFINITY ? 0.0f : ex2_approx(M - top);
-                    const float w = mk == -INFINITY ? 0.0f : ex2_approx(mk - top);
-                    M = top;
-                    l = l * old + lk * w;
-                    acc.scale(old);
-                    const float *r = slot + part[q].row * kD;
-#pragma unroll 8
-                    for (int k = 0; k < n; k++)
-                        acc.fma_row(r + static_cast<int64_t>(k) * kSlot, lane, __shfl_sync(0xFFFFFFFFu, w, k));
+                for (int d = 1; d < 32; d <<= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                top = fmaxf(top, M);
+                const float old = M == -INFINITY ? 0.0f : ex2_approx(M - top);
+                const float w = mk == -INFINITY ? 0.0f : ex2_approx(mk - top);
+                M = top;
+                l = l * old + lk * w;
+                acc.scale(old);
+#pragma unroll 1
+                for (int c = 0;;) {
+#pragma unroll
+                    for (int k = 0; k < kChunk; k++)
+                        if (c + k < n)
+                            acc.fma(x[k], __shfl_sync(0xFFFFFFFFu, w, c + k));
+                    c += kChunk;
+                    if (c >= n)
+                        break;
+#pragma unroll
+                    for (int k = 0; k < kChunk; k++)
+                        if (c + k < n)
+                            x[k].load_row(slot_of(k0 + c + k, kD), lane);
                 }
             }
 #pragma unroll
@@ -207,7 +231,9 @@ __global__ void __launch_bounds__(32 * (kWide ? kRowWarpsWide : kRowWarps))
                     for (int w = 0; w < kWarps; w++) {
                         const float f = part_m[w] == -INFINITY ? 0.0f : ex2_approx(part_m[w] - M);
                         l += part_l[w] * f;
-                        acc.fma_row(part_o[w], lane, f);
+                        RowVec<kD> x;
+                        x.load_row(part_o[w], lane);
+                        acc.fma(x, f);
                     }
                 }
                 __syncthreads();
