@@ -434,3 +434,85 @@ def test_step_rope_appends_behind_empty_lengths(cuda_device, with_mass):
         want = torch.ones(S, 2, 16)
         want[:, :, 3] = 0.0
         assert torch.equal(mass.cpu(), want)
+
+
+def test_calls_on_two_streams_at_once(cuda_device):
+    """Prefix decodes (tensor cores and plan) and decodes with weights in flight together, each stream with
+    its own workspaces, outputs and masses: the bits of one call at a time."""
+    from bit_paged_kv_block_b200 import saw
+    dev = cuda_device
+    lens = [(29 * s) % 120 for s in range(64)]
+    wl, pages, scales, q, mass = _case([1100] + lens, 16, 1, 128, seed=91)
+    kv, sc = device_cache_from(pages, scales, dev)
+    table = torch.from_numpy(wl.block_table).to(dev)
+    own, prefix = table[1:].contiguous(), table[0].contiguous()
+    dlens, dq = torch.tensor(lens, dtype=torch.int32, device=dev), q[1:].contiguous().to(dev)
+
+    def buffers():
+        return ([torch.full((64, 16, 128), float("nan"), dtype=torch.bfloat16, device=dev) for _ in range(3)],
+                saw.allocate_prefix_workspace(1, 16, 64, 1100, dev), saw.allocate_prefix_workspace(1, 16, 64, 1100, dev),
+                saw.allocate_mass_workspace(1, 16, 64, own.shape[1], dev), torch.from_numpy(mass.copy()).to(dev))
+
+    def run(b, stream=None):
+        out, ws, ws2, wm, dm = b
+        saw.saw_paged_decode_attn_prefix(dq, kv, sc, prefix, 1100, own, dlens, out[0], ws, stream=stream)
+        saw.saw_paged_decode_attn_prefix(dq, kv, sc, prefix, 40, own, dlens, out[1], ws2, stream=stream)
+        saw.saw_paged_decode_attn_mass(dq, kv, sc, dm, own, dlens, out[2], wm, stream=stream)
+
+    want = buffers()
+    run(want)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[buffers() for _ in range(8)] for _ in streams]
+    torch.cuda.synchronize()
+    for k in range(8):
+        for st, b in zip(streams, got):
+            run(b[k], st)
+    torch.cuda.synchronize()
+    for b in got[0] + got[1]:
+        for x, y in zip(b[0], want[0]):
+            assert torch.equal(x, y)
+        assert torch.equal(b[4], want[4])
+
+
+def test_two_graphs_share_a_workspace(cuda_device):
+    """Two captured calls of different sizes over one workspace, replayed in turn on one stream."""
+    from bit_paged_kv_block_b200 import saw
+    dev = cuda_device
+    lens = [300, 17, 0, 64, 1000]
+    wl, pages, scales, q, mass = _case(lens, 8, 2, 128, seed=92)
+    kv, sc = device_cache_from(pages, scales, dev)
+    table = torch.from_numpy(wl.block_table).to(dev)
+    dlens, dq = torch.tensor(lens, dtype=torch.int32, device=dev), q.to(dev)
+    ws = saw.allocate_mass_workspace(2, 8, 5, table.shape[1], dev)
+    wp = saw.allocate_prefix_workspace(2, 8, 5, 600, dev)
+    dm0 = torch.from_numpy(mass.copy()).to(dev)     # outlives both graphs
+    jobs = []
+    for n, prefix in ((5, 600), (2, 33)):
+        out = [torch.empty(n, 8, 128, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+        dm = torch.from_numpy(mass.copy()).to(dev)
+        args = dq[:n].contiguous(), table[:n].contiguous(), dlens[:n].contiguous()
+
+        def call(out=out, dm=dm, args=args, prefix=prefix):
+            dm.copy_(dm0)
+            saw.saw_paged_decode_attn_mass(args[0], kv, sc, dm, args[1], args[2], out[0], ws)
+            saw.saw_paged_decode_attn_prefix(args[0], kv, sc, table[4], prefix, args[1], args[2], out[1], wp)
+        call()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (*out, dm)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        jobs.append((graph, (*out, dm), want))
+    for _ in range(3):
+        for graph, got, _ in jobs:
+            for t in got:
+                t.fill_(float("nan"))
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, got, want in jobs:
+            for x, y in zip(got, want):
+                same = torch.equal(x, y)
+                assert same
+    for graph, _, _ in jobs:
+        graph.reset()
