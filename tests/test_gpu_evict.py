@@ -516,3 +516,38 @@ def test_two_graphs_share_a_workspace(cuda_device):
                 assert same
     for graph, _, _ in jobs:
         graph.reset()
+
+
+@pytest.mark.parametrize("bits", [0x7E00, 0x7C00, 0xFBFF])
+def test_slots_past_the_ends_are_never_read_into_results(cuda_device, bits):
+    """NaN, infinite and largest scales and zeros behind a sequence's last token (and a prefix's): the same
+    bits as with zeros there, and no mass for them."""
+    from bit_paged_kv_block_b200 import saw
+    dev = cuda_device
+    for hq, hkv, d, first in ((16, 1, 128, 1101), (8, 2, 128, 37), (6, 2, 64, 21), (12, 1, 256, 40)):
+        lens = [first] + [(17 * s) % 90 for s in range(64 if first == 1101 else 9)]
+        wl, pages, scales, q, mass = _case(lens, hq, hkv, d, seed=first)
+        table = torch.from_numpy(wl.block_table).to(dev)
+        dlens, dq = torch.tensor(lens, dtype=torch.int32, device=dev), q.to(dev)
+        S = len(lens) - 1
+        results = []
+        for fill in (0, bits):
+            sc_np, code = scales.copy().view(np.uint16), pages.copy()
+            for s, n in enumerate(lens):
+                for t in range(n, (n + 15) // 16 * 16):
+                    sc_np[wl.block_table[s, t // 16], :, :, t % 16] = fill
+                    code[wl.block_table[s, t // 16], :, :, t % 16] = 0xFF if fill else 0
+            kv, sc = device_cache_from(code, sc_np.view(scales.dtype), dev)
+            out = [torch.empty(S + 1, hq, d, dtype=torch.bfloat16, device=dev),
+                   torch.empty(S, hq, d, dtype=torch.bfloat16, device=dev)]
+            dm = torch.from_numpy(mass.copy()).to(dev)
+            saw.saw_paged_decode_attn_mass(dq, kv, sc, dm, table, dlens, out[0],
+                                           saw.allocate_mass_workspace(hkv, hq, S + 1, table.shape[1], dev, head_dim=d))
+            saw.saw_paged_decode_attn_prefix(dq[1:].contiguous(), kv, sc, table[0].contiguous(), first,
+                                             table[1:].contiguous(), dlens[1:].contiguous(), out[1],
+                                             saw.allocate_prefix_workspace(hkv, hq, S, first, dev, head_dim=d))
+            torch.cuda.synchronize()
+            results.append((*out, dm))
+        for x, y in zip(*results):
+            same, finite = torch.equal(x, y), bool(torch.isfinite(y.float()).all())
+            assert same and finite, f"{hq}/{hkv}/{d}"
