@@ -423,7 +423,8 @@ typedef struct saw_rope {
  * num_q_heads = 0 (q, q_out unused) rotates and appends keys alone.  mass (or NULL): the accumulated
  * weights below, fp32 [num_pages][Hkv][16], set to 0 at the new slots.  A token with a negative slot,
  * a slot out of range (SAW_DEV_BAD_SLOT) or a position outside the table (SAW_DEV_BAD_POSITION) is
- * skipped as a whole: its q_out row, cache rows and masses keep what they held.
+ * skipped as a whole: its q_out row, cache rows and masses keep what they held.  Two tokens of a call
+ * must not name the same slot (it would hold parts of either).
  * The _plain variant is the append of a plain INT4 cache (no Hadamard rotation). */
 int saw_rope_rotate_quantize_paged(const saw_cache_desc *cache, const saw_rope *rope,
                                    int32_t num_q_heads, const void *q, int64_t q_stride,
@@ -480,9 +481,9 @@ int saw_paged_decode_attn_prefix_plain(const saw_cache_desc *cache, int32_t num_
  * saw_paged_decode_attn_mass: saw_paged_decode_attn with a bf16 output ([S][Hq][D], rounded once)
  * that also adds, for every token t < seq_lens[s] of every sequence and kv head h,
  *     mass[page][h][t mod 16] += sum over the G query heads of h of softmax(logits)_t.
- * The weights are accurate to fp32's precision.  Each mass gets one add per sequence of the call that
- * holds its page, so results repeat bit for bit unless sequences share a page, whose adds then happen
- * in either order.  Slots past a sequence's end are not touched.  workspace: at least
+ * The weights are accurate to fp32's precision.  Each mass gets one add per entry of the block table
+ * that names its page, so results repeat bit for bit unless a page is named twice (by two sequences, or
+ * by one), whose adds then happen in either order.  Slots past a sequence's end are not touched.  workspace: at least
  * saw_paged_decode_mass_workspace_bytes() (it holds the logits of every page that the block table can
  * name), 256-byte aligned, no initialisation needed. */
 size_t saw_paged_decode_mass_workspace_bytes(const saw_cache_desc *cache, int32_t num_q_heads,
