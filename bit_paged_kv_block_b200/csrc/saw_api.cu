@@ -990,6 +990,8 @@ static int check_decode_bf16_out(const saw_cache_desc *cache, int32_t num_q_head
     if (!aligned(q, 16) || !aligned(kv_pages, 16) || !aligned(scales, 16) || !aligned(out, 16) ||
         !aligned(block_table, 4) || !aligned(seq_lens, 4))
         return SAW_ERR_INVALID_ARGUMENT;
+    if (out == q)
+        return SAW_ERR_INVALID_ARGUMENT;   // rows of q are read while others of out are written
     // query rows (num_seqs * num_q_heads) are counted in 32 bits
     if (int64_t(num_seqs) * num_q_heads > (int64_t(1) << 30))
         return SAW_ERR_UNSUPPORTED;
@@ -1251,6 +1253,8 @@ int saw_decode_step_rope_mass(const saw_cache_desc *cache, const saw_rope *rope,
                            seq_lens, num_seqs, sm_scale, out, workspace, workspace_bytes);
     if (rc != SAW_OK || num_seqs == 0)
         return rc;
+    if (out == q)
+        return SAW_ERR_INVALID_ARGUMENT;
     rc = rope_append_impl(cache, rope, num_q_heads, q, 0, k_new, 0, v_new, 0, positions, slot_mapping, num_seqs,
                           q_rot, kv_pages, scales, mass, dev_status, stream, true);
     if (rc != SAW_OK)

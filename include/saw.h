@@ -454,7 +454,7 @@ int saw_rope_quantize_paged_plain(const saw_cache_desc *cache, const saw_rope *r
  * it is infinite, and a weight below 2^-23 of its row's largest counts as 0.
  * workspace: at least saw_paged_decode_prefix_workspace_bytes() for these sizes (a larger num_seqs or
  * prefix_len covers a smaller one at the same heads), 256-byte aligned, no initialisation needed.
- * 0 <= prefix_len <= 2^30. */
+ * 0 <= prefix_len <= 2^30; out must not be q. */
 size_t saw_paged_decode_prefix_workspace_bytes(const saw_cache_desc *cache, int32_t num_q_heads,
                                                int32_t num_seqs, int32_t prefix_len);
 int saw_paged_decode_attn_prefix(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
@@ -485,7 +485,7 @@ int saw_paged_decode_attn_prefix_plain(const saw_cache_desc *cache, int32_t num_
  * that names its page, so results repeat bit for bit unless a page is named twice (by two sequences, or
  * by one), whose adds then happen in either order.  Slots past a sequence's end are not touched.  workspace: at least
  * saw_paged_decode_mass_workspace_bytes() (it holds the logits of every page that the block table can
- * name), 256-byte aligned, no initialisation needed. */
+ * name), 256-byte aligned, no initialisation needed.  out must not be q. */
 size_t saw_paged_decode_mass_workspace_bytes(const saw_cache_desc *cache, int32_t num_q_heads,
                                              int32_t num_seqs, int32_t max_blocks_per_seq);
 int saw_paged_decode_attn_mass(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
@@ -526,7 +526,7 @@ int saw_evict_paged(const saw_cache_desc *cache, uint8_t *kv_pages, void *scales
  * cache hold), then the decode of q_rot (bf16 [S][Hq][D], written by the append), launched as a
  * programmatic dependent.  saw_decode_step_rope decodes with saw_paged_decode_attn (fp32 out, its
  * workspace); saw_decode_step_rope_mass with saw_paged_decode_attn_mass (bf16 out, its workspace),
- * the append clearing the new slots' masses. */
+ * the append clearing the new slots' masses; its out must be neither q nor q_rot. */
 int saw_decode_step_rope(const saw_cache_desc *cache, const saw_rope *rope, int32_t num_q_heads,
                          const void *q, const void *k_new, const void *v_new,
                          const int64_t *positions, const int64_t *slot_mapping, void *q_rot,

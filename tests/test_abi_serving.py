@@ -87,14 +87,14 @@ def test_rope_append_checks():
     assert _append(T=0, q=0, k=0, v=0, pos=0, slots=0, q_out=0, pages=0, scales=0) == OK
 
 
-def _prefix(desc=None, hq=32, S=2, q=16, table=16, prefix=40, bt=16, lens=16, out=16, ws=256, ws_bytes=16,
+def _prefix(desc=None, hq=32, S=2, q=16, table=16, prefix=40, bt=16, lens=16, out=32, ws=256, ws_bytes=16,
             max_blocks=4, sm_scale=0.1):
     return saw.lib.saw_paged_decode_attn_prefix(
         ctypes.byref(desc or _desc()), hq, P(q), P(16), P(16), P(table), prefix, P(bt), max_blocks, P(lens),
         S, sm_scale, P(out), P(ws), ws_bytes, None, None)
 
 
-def _mass(desc=None, hq=32, S=2, q=16, mass=16, bt=16, lens=16, out=16, ws=256, ws_bytes=16, max_blocks=4,
+def _mass(desc=None, hq=32, S=2, q=16, mass=16, bt=16, lens=16, out=32, ws=256, ws_bytes=16, max_blocks=4,
           sm_scale=0.1):
     return saw.lib.saw_paged_decode_attn_mass(
         ctypes.byref(desc or _desc()), hq, P(q), P(16), P(16), P(mass), P(bt), max_blocks, P(lens), S,
@@ -113,6 +113,7 @@ def test_bf16_decode_checks(call):
     assert call(q=0) == INVALID
     assert call(q=8) == INVALID
     assert call(out=8) == INVALID
+    assert call(out=16) == INVALID                                     # out is q
     assert call(bt=2) == INVALID
     assert call(lens=0) == INVALID
     assert call(max_blocks=0) == INVALID
@@ -171,7 +172,7 @@ def test_evict_checks():
 def test_steps_check_both_halves():
     d, r = _desc(), _rope()
 
-    def call(fn, q=16, q_rot=32, out=16, extra=()):
+    def call(fn, q=16, q_rot=32, out=48, extra=()):
         return fn(ctypes.byref(d), ctypes.byref(r), 32, P(q), P(16), P(16), P(16), P(16), P(q_rot), P(16), P(16),
                   *extra, P(16), 4, P(16), 2, 0.1, P(out), P(256), 16, None, None)
     assert call(saw.lib.saw_decode_step_rope, q=0) == INVALID
@@ -180,6 +181,7 @@ def test_steps_check_both_halves():
     assert call(saw.lib.saw_decode_step_rope_mass, q=0, extra=(P(16),)) == INVALID
     assert call(saw.lib.saw_decode_step_rope_mass, extra=(P(0),)) == INVALID     # needs the masses
     assert call(saw.lib.saw_decode_step_rope_mass, out=8, extra=(P(16),)) == INVALID
+    assert call(saw.lib.saw_decode_step_rope_mass, out=32, extra=(P(16),)) == INVALID    # out is q_rot
 
 
 def test_status_bits_and_strings():
