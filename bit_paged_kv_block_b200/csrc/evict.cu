@@ -397,6 +397,9 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream)
     const int64_t most = static_cast<int64_t>(a.max_blocks) * kPageSize;
     const int64_t segments = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
 
+    static SmemCache cache;
+    static const void *const kernels[] = {reinterpret_cast<const void *>(evict_select_kernel<256>),
+                                          reinterpret_cast<const void *>(evict_select_kernel<1024>)};
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
@@ -410,7 +413,7 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream)
     p.smem_keys = static_cast<int32_t>(std::min<int64_t>(chunk, kSelSmemKeys));
     auto *select = chunk <= 4096 ? evict_select_kernel<256> : evict_select_kernel<1024>;
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemKeys * 4);
+        e = raise_smem(cache, kernels, 2, kSelSmemKeys * 4);
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute attr[1];

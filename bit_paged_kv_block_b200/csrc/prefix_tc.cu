@@ -648,7 +648,10 @@ cudaError_t launch_prefix_tc(const DecodeArgs &a, const int32_t *prefix_table, i
     // q carries sm_scale * log2(e) and 1/sqrt(128) of the unnormalised butterfly
     p.q_mult = static_cast<float>((a.rotate ? static_cast<double>(kHadC) : 1.0) * a.sm_scale * 1.4426950408889634);
     auto *kernel = a.rotate ? prefix_tc_kernel<true> : prefix_tc_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPtSmem));
+    static SmemCache cache;
+    static const void *const kernels[] = {reinterpret_cast<const void *>(prefix_tc_kernel<true>),
+                                          reinterpret_cast<const void *>(prefix_tc_kernel<false>)};
+    const cudaError_t e = raise_smem(cache, kernels, 2, kPtSmem);
     if (e != cudaSuccess)
         return e;
     kernel<<<static_cast<unsigned>(s.splits * s.row_pairs * p.hkv), kPtThreads, kPtSmem, stream>>>(p);

@@ -519,12 +519,14 @@ cudaError_t launch(const RopeAppendArgs &a, RopeParams &p, const CUtensorMap &tk
     constexpr size_t kSmem = rq_smem_bytes<kD>();
     static_assert(RqDims<kD>::kStageBytes == 4096, "the ring's stages hold a 32-row tile");
     auto *kernel = rope_append_kernel<kRotate, kD>;
+    static SmemCache cache;   // (of this instantiation's kernel)
+    const void *const entry = reinterpret_cast<const void *>(kernel);
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+        e = raise_smem(cache, &entry, 1, kSmem);
     if (e != cudaSuccess)
         return e;
     // 4 CTAs per SM in all, shared out by what a 64-element row costs: a k or v row about twice a

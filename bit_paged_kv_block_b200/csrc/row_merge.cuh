@@ -3,7 +3,6 @@
 #pragma once
 
 #include <algorithm>
-#include <mutex>
 
 #include "int4_format.cuh"
 
@@ -250,32 +249,6 @@ __global__ void __launch_bounds__(32 * (kWide ? kRowWarpsWide : kRowWarps))
                 p.lse[out_row] = M + log2f(l);
         }
     }
-}
-
-// Dynamic shared memory that kernels may use, raised per device as calls need it.  One cache per set of
-// kernels, whatever decode kernels they follow: the attribute is the kernel's, and a second cache would
-// lower what the first had raised.
-struct SmemCache {
-    std::mutex mu;
-    size_t bytes[ShapeCache::kMaxDevices] = {};
-};
-
-inline cudaError_t raise_smem(SmemCache &cache, const void *const *kernels, int count, size_t bytes)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess)
-        return e;
-    if (dev < 0 || dev >= ShapeCache::kMaxDevices)
-        return cudaErrorInvalidDevice;
-    std::lock_guard<std::mutex> lock(cache.mu);
-    if (bytes <= cache.bytes[dev])
-        return cudaSuccess;
-    for (int k = 0; k < count && e == cudaSuccess; k++)
-        e = cudaFuncSetAttribute(kernels[k], cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e == cudaSuccess)
-        cache.bytes[dev] = bytes;
-    return e;
 }
 
 template <int kD, int kMode>

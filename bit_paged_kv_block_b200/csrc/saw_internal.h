@@ -5,8 +5,36 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
+#include <mutex>
 
 namespace saw {
+
+// Dynamic shared memory that kernels may use, raised per device as calls need it.  One cache per set of
+// kernels, whatever decode kernels they follow: the attribute is the kernel's, and a second cache would
+// lower what the first had raised.
+struct SmemCache {
+    static constexpr int kMaxDevices = 64;
+    std::mutex mu;
+    size_t bytes[kMaxDevices] = {};
+};
+
+inline cudaError_t raise_smem(SmemCache &cache, const void *const *kernels, int count, size_t bytes)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= SmemCache::kMaxDevices)
+        return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(cache.mu);
+    if (bytes <= cache.bytes[dev])
+        return cudaSuccess;
+    for (int k = 0; k < count && e == cudaSuccess; k++)
+        e = cudaFuncSetAttribute(kernels[k], cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess)
+        cache.bytes[dev] = bytes;
+    return e;
+}
 
 // cuTensorMapEncodeTiled from the driver, looked up through the runtime (no libcuda link).
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()

@@ -184,12 +184,14 @@ def _ptr(t):
 
 # the current stream's handle without building a Stream object (3 us a call), where torch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# the current device of an initialised CUDA context
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_current_device() if torch.cuda.is_initialized() else torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -707,7 +709,7 @@ def saw_rope_table(table, scaling: saw_rope_scaling, first_position: int = 0, st
     position first_position + r."""
     _present("table", table)
     _need_here((table, "table", torch.float32, 2))
-    rc = lib.saw_rope_table(_ptr(table), int(first_position), table.shape[0], table.shape[1],
+    rc = lib.saw_rope_table(table.data_ptr(), int(first_position), table.shape[0], table.shape[1],
                             ctypes.byref(scaling), _stream(stream))
     _check(rc, "saw_rope_table")
 
@@ -715,7 +717,7 @@ def saw_rope_table(table, scaling: saw_rope_scaling, first_position: int = 0, st
 def _need_here(*specs) -> int:
     """_need for (tensor or None, name, dtype, dimensions) of one call, whose tensors must all be on
     the current CUDA device: the library launches there.  Returns that device."""
-    device = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    device = _current_device() if torch.cuda.is_initialized() else -2
     for t, name, dtype, ndim in specs:
         if t is None:
             continue
@@ -817,8 +819,8 @@ def saw_rope_rotate_quantize_paged(q, k, v, positions, slot_mapping, rope, q_out
     desc = _cache_of(kv_pages, scales, mass)
     T, hq, qs, ks, vs, rp = _rope_rows(q, k, v, positions, slot_mapping, q_out, rope, desc, device)
     fn = lib.saw_rope_rotate_quantize_paged if rotate else lib.saw_rope_quantize_paged_plain
-    rc = fn(ctypes.byref(desc), ctypes.byref(rp), hq, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
-            _ptr(positions), _ptr(slot_mapping), T, _ptr(q_out), _ptr(kv_pages), _ptr(scales),
+    rc = fn(ctypes.byref(desc), ctypes.byref(rp), hq, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+            positions.data_ptr(), slot_mapping.data_ptr(), T, _ptr(q_out), kv_pages.data_ptr(), scales.data_ptr(),
             _ptr(mass), _ptr(dev_status), _stream(stream))
     _check(rc, "saw_rope_rotate_quantize_paged" if rotate else "saw_rope_quantize_paged_plain")
 
@@ -872,9 +874,9 @@ def saw_paged_decode_attn_prefix(q, kv_pages, scales, prefix_table, prefix_len, 
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(desc.head_dim)
     fn = lib.saw_paged_decode_attn_prefix if rotate else lib.saw_paged_decode_attn_prefix_plain
-    rc = fn(ctypes.byref(desc), hq, _ptr(q), _ptr(kv_pages), _ptr(scales), _ptr(prefix_table),
-            prefix_len, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), S, float(sm_scale),
-            _ptr(out), _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream))
+    rc = fn(ctypes.byref(desc), hq, _ptr(q), kv_pages.data_ptr(), scales.data_ptr(), _ptr(prefix_table),
+            prefix_len, block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), S, float(sm_scale),
+            out.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(dev_status), _stream(stream))
     _check(rc, "saw_paged_decode_attn_prefix" if rotate else "saw_paged_decode_attn_prefix_plain")
 
 
@@ -907,9 +909,9 @@ def saw_paged_decode_attn_mass(q, kv_pages, scales, mass, block_table, seq_lens,
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(desc.head_dim)
     fn = lib.saw_paged_decode_attn_mass if rotate else lib.saw_paged_decode_attn_mass_plain
-    rc = fn(ctypes.byref(desc), hq, _ptr(q), _ptr(kv_pages), _ptr(scales), _ptr(mass),
-            _ptr(block_table), block_table.shape[1], _ptr(seq_lens), S, float(sm_scale), _ptr(out),
-            _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream))
+    rc = fn(ctypes.byref(desc), hq, _ptr(q), kv_pages.data_ptr(), scales.data_ptr(), _ptr(mass),
+            block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), S, float(sm_scale), out.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), _ptr(dev_status), _stream(stream))
     _check(rc, "saw_paged_decode_attn_mass" if rotate else "saw_paged_decode_attn_mass_plain")
 
 
@@ -931,9 +933,9 @@ def saw_evict_paged(kv_pages, scales, mass, block_table, seq_lens, new_table, ne
         raise ValueError("block_table, new_table and new_lens need one row per sequence")
     if tuple(kept.shape[:2]) != (S, desc.num_kv_heads):
         raise ValueError("kept must be [S][Hkv][keep]")
-    rc = lib.saw_evict_paged(ctypes.byref(desc), _ptr(kv_pages), _ptr(scales), _ptr(mass),
-                             _ptr(block_table), block_table.shape[1], _ptr(seq_lens), S,
-                             _ptr(new_table), new_table.shape[1], _ptr(new_lens), _ptr(kept),
+    rc = lib.saw_evict_paged(ctypes.byref(desc), kv_pages.data_ptr(), scales.data_ptr(), _ptr(mass),
+                             block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), S,
+                             new_table.data_ptr(), new_table.shape[1], new_lens.data_ptr(), kept.data_ptr(),
                              kept.shape[2], int(sink), int(recent), _ptr(dev_status),
                              _stream(stream))
     _check(rc, "saw_evict_paged")
@@ -958,8 +960,8 @@ def saw_decode_step_rope(q, k_new, v_new, positions, slot_mapping, rope, q_rot, 
     rp = _rope_rows(q, k_new, v_new, positions, slot_mapping, q_rot, rope, desc, device)[-1]
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(desc.head_dim)
-    head = (ctypes.byref(desc), ctypes.byref(rp), q.shape[1], _ptr(q), _ptr(k_new), _ptr(v_new),
-            _ptr(positions), _ptr(slot_mapping), _ptr(q_rot), _ptr(kv_pages), _ptr(scales))
+    head = (ctypes.byref(desc), ctypes.byref(rp), q.shape[1], _ptr(q), k_new.data_ptr(), v_new.data_ptr(),
+            positions.data_ptr(), slot_mapping.data_ptr(), q_rot.data_ptr(), kv_pages.data_ptr(), scales.data_ptr())
     if mass is None:
         S = _decode_checks(q_rot, kv_pages, scales, block_table, seq_lens, out, workspace,
                            dev_status)[1]
@@ -969,6 +971,6 @@ def saw_decode_step_rope(q, k_new, v_new, positions, slot_mapping, rope, q_rot, 
                              mass)[1]
         head += (_ptr(mass),)
         fn, name = lib.saw_decode_step_rope_mass, "saw_decode_step_rope_mass"
-    rc = fn(*head, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), S, float(sm_scale),
-            _ptr(out), _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream))
+    rc = fn(*head, block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), S, float(sm_scale),
+            out.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(dev_status), _stream(stream))
     _check(rc, name)
