@@ -8,14 +8,17 @@
 // sequences, and go back to the allocator afterwards.
 //
 // Two kernels.  The selection (a CTA per sequence and kv head, or a cluster of up to 8 that share its
-// tokens where there are few) holds the masses in shared memory as integer keys (non-negative floats order as their bits) and narrows [lo, hi) around the need-th
-// largest: a histogram of the range in 1024 bins, the bin that holds it, again; at most 4 passes, and
-// since the range starts at the masses' own, the bins are spread over and their counters rarely
-// collide.  Then it writes the kept tokens' indices in order.  The move (a warp per new page and kv
-// head) gathers the rows.  Both are bound by the bytes of the masses and of the kept rows.
+// tokens where there are few) holds the masses in shared memory as integer keys (non-negative floats
+// order as their bits) and narrows [lo, hi] around the need-th largest: a histogram of the range in
+// 1024 bins, the bin that holds it, again; at most 4 passes, and since the range starts at the masses'
+// own, the bins are spread over and their counters rarely collide.  Then it writes the kept tokens'
+// indices in order.  The move (a warp per new page and kv head) gathers the rows.  64 sequences of up to
+// 4096 tokens x 8 kv heads to 2048: selections 21 us, move 58 us (5 TB/s read and written, in rows of 64
+// bytes); 1 of 32768 to 8192: 22.5 us in all, most of it the selection's passes, each a cluster barrier.
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "saw_device.cuh"
 #include "saw_internal.h"
@@ -347,7 +350,8 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictParams p)
             const int64_t from = __shfl_sync(0xFFFFFFFFu, src, row & 15);
             live[i] = from >= 0;
             if (live[i])
-                w[i] = ldg_stream16(p.kv_pages + (from + half * kPageSize) * kRowBytes_ + 16 * (lane % kLanes));
+                w[i] = __ldcg(reinterpret_cast<const uint4 *>(p.kv_pages + (from + half * kPageSize) * kRowBytes_ +
+                                                              16 * (lane % kLanes)));
         }
         const uint32_t *sc = reinterpret_cast<const uint32_t *>(p.scales);
         uint32_t pair = 0;
@@ -370,6 +374,26 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictParams p)
                 p.mass[(dst / (2 * kPageSize)) * kPageSize + lane] = m;
         }
     }
+}
+
+// CTAs of the move that an SM holds at once, which is how many it gets: 64 x 4096 tokens take 79.4 us in one
+// wave (5 CTAs at D = 128), 4 more with 8 CTAs an SM, 3 more with 3 or 4, and 14 more with registers capped
+// so that 6 fit at once.  (Streaming stores cost 14 us, streaming loads 2.)
+template <int kD>
+cudaError_t move_residency(int dev, int &ctas)
+{
+    static std::atomic<int> known[SmemCache::kMaxDevices];
+    if (dev < 0 || dev >= SmemCache::kMaxDevices)
+        return cudaErrorInvalidDevice;
+    ctas = known[dev].load(std::memory_order_relaxed);
+    if (ctas > 0)
+        return cudaSuccess;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, evict_move_kernel<kD>, 256, 0);
+    if (e != cudaSuccess)
+        return e;
+    ctas = std::max(1, ctas);
+    known[dev].store(ctas, std::memory_order_relaxed);
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -430,9 +454,15 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream)
     if ((e = cudaLaunchKernelEx(&cfg, select, p)) != cudaSuccess)
         return e;
     const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * ((a.keep + kPageSize - 1) / kPageSize);
+    int resident = 0;
+    e = a.head_dim == 64    ? move_residency<64>(dev, resident)
+        : a.head_dim == 128 ? move_residency<128>(dev, resident)
+                            : move_residency<256>(dev, resident);
+    if (e != cudaSuccess)
+        return e;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((units + 7) / 8, 8 * sms)));
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((units + 7) / 8, static_cast<int64_t>(resident) * sms)));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     e = a.head_dim == 64    ? cudaLaunchKernelEx(&cfg, evict_move_kernel<64>, p)
