@@ -143,6 +143,10 @@ __global__ void __launch_bounds__(32 * (kWide ? kRowWarpsWide : kRowWarps))
         return {p.partials + (tb.spre[s] + j + u_lo) * kSlot, static_cast<int>(u_hi - u_lo) + 1, row};
     };
     pdl_wait();
+    // the accumulation's CTAs find their places while a small merge runs (3 sequences of 333 tokens: 16.0 us,
+    // else 17.2); beside a large one they take its CTAs' issue slots (64 x 8192: 98.7 and 98.0)
+    if (!kPrefix && gridDim.x <= 148)
+        pdl_launch_dependents();
     const int nb = (p.group + kRowsPerBlock - 1) / kRowsPerBlock;
     const int segments = p.batch * p.hkv * nb;
     for (int64_t o = blockIdx.x; o < (kWide ? static_cast<int64_t>(segments) * kRowsPerBlock : segments); o += gridDim.x) {
