@@ -767,6 +767,16 @@ int saw_decode_step_window(const saw_cache_desc *cache, const saw_window_cache *
 
 // ---- rotary positions ------------------------------------------------------------------------
 
+// The status of a launch.  A failed call's error is taken off the runtime's record, where the next call's
+// check of its own launch would find it.
+static int cuda_status(cudaError_t e)
+{
+    if (e == cudaSuccess)
+        return SAW_OK;
+    cudaGetLastError();
+    return SAW_ERR_CUDA;
+}
+
 // Frequencies of a rotary embedding in turns per position, and its amplitude (saw.h); false for
 // scaling parameters out of range.
 static bool rope_turns(const saw_rope_scaling &sc, int32_t rotary_dim, double *turns, double &amplitude)
@@ -844,7 +854,7 @@ int saw_rope_table(float *table, int64_t first_position, int64_t num_positions, 
     a.first_position = first_position;
     a.num_positions = num_positions;
     a.rotary_dim = rotary_dim;
-    return saw::launch_rope_table(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
+    return cuda_status(saw::launch_rope_table(a, static_cast<cudaStream_t>(stream)));
 }
 
 static int check_rope(const saw_cache_desc *cache, const saw_rope *rope)
@@ -932,7 +942,7 @@ static int rope_append_impl(const saw_cache_desc *cache, const saw_rope *rope, i
     a.rotary_dim = rope->rotary_dim;
     a.interleaved = rope->interleaved != 0;
     a.mass = mass;
-    return saw::launch_rope_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
+    return cuda_status(saw::launch_rope_append(a, static_cast<cudaStream_t>(stream)));
 }
 
 int saw_rope_rotate_quantize_paged(const saw_cache_desc *cache, const saw_rope *rope,
@@ -1001,7 +1011,7 @@ static int check_decode_bf16_out(const saw_cache_desc *cache, int32_t num_q_head
 static int check_workspace(size_t need, const void *workspace, size_t workspace_bytes)
 {
     if (need == 0)
-        return SAW_ERR_CUDA;
+        return cuda_status(cudaErrorUnknown);
     return workspace != nullptr && workspace_bytes >= need && aligned(workspace, 256) ? SAW_OK
                                                                                      : SAW_ERR_WORKSPACE;
 }
@@ -1019,8 +1029,11 @@ size_t saw_paged_decode_prefix_workspace_bytes(const saw_cache_desc *cache, int3
 {
     if (!decode_sizes_ok(cache, num_q_heads, num_seqs) || prefix_len < 0 || prefix_len > (1 << 30))
         return 0;
-    return saw::decode_prefix_workspace_bytes(cache->num_kv_heads, num_q_heads, num_seqs, prefix_len,
-                                              cache->head_dim);
+    const size_t n = saw::decode_prefix_workspace_bytes(cache->num_kv_heads, num_q_heads, num_seqs, prefix_len,
+                                                        cache->head_dim);
+    if (n == 0)
+        cudaGetLastError();
+    return n;
 }
 
 static int decode_prefix_impl(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
@@ -1050,10 +1063,7 @@ static int decode_prefix_impl(const saw_cache_desc *cache, int32_t num_q_heads, 
                                     dev_status);
     a.out_bf16 = out;
     a.rotate = rotate;
-    return saw::launch_paged_decode_prefix(a, prefix_table, prefix_len, static_cast<cudaStream_t>(stream)) ==
-                   cudaSuccess
-               ? SAW_OK
-               : SAW_ERR_CUDA;
+    return cuda_status(saw::launch_paged_decode_prefix(a, prefix_table, prefix_len, static_cast<cudaStream_t>(stream)));
 }
 
 int saw_paged_decode_attn_prefix(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
@@ -1088,8 +1098,11 @@ size_t saw_paged_decode_mass_workspace_bytes(const saw_cache_desc *cache, int32_
     if (!decode_sizes_ok(cache, num_q_heads, num_seqs) || max_blocks_per_seq <= 0 ||
         int64_t(max_blocks_per_seq) * 16 > INT32_MAX)
         return 0;
-    return saw::decode_mass_workspace_bytes(cache->num_kv_heads, num_q_heads, num_seqs, max_blocks_per_seq,
-                                            cache->head_dim);
+    const size_t n = saw::decode_mass_workspace_bytes(cache->num_kv_heads, num_q_heads, num_seqs,
+                                                      max_blocks_per_seq, cache->head_dim);
+    if (n == 0)
+        cudaGetLastError();
+    return n;
 }
 
 static int check_decode_mass(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
@@ -1121,9 +1134,7 @@ static int decode_mass_impl(const saw_cache_desc *cache, int32_t num_q_heads, co
                                     dev_status);
     a.out_bf16 = out;
     a.rotate = rotate;
-    return saw::launch_paged_decode_mass(a, mass, static_cast<cudaStream_t>(stream), programmatic) == cudaSuccess
-               ? SAW_OK
-               : SAW_ERR_CUDA;
+    return cuda_status(saw::launch_paged_decode_mass(a, mass, static_cast<cudaStream_t>(stream), programmatic));
 }
 
 int saw_paged_decode_attn_mass(const saw_cache_desc *cache, int32_t num_q_heads, const void *q,
@@ -1206,7 +1217,7 @@ int saw_evict_paged(const saw_cache_desc *cache, uint8_t *kv_pages, void *scales
     a.sink = sink;
     a.recent = recent;
     a.status = dev_status;
-    return saw::launch_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SAW_OK : SAW_ERR_CUDA;
+    return cuda_status(saw::launch_evict(a, static_cast<cudaStream_t>(stream)));
 }
 
 int saw_decode_step_rope(const saw_cache_desc *cache, const saw_rope *rope, int32_t num_q_heads,
@@ -1232,8 +1243,7 @@ int saw_decode_step_rope(const saw_cache_desc *cache, const saw_rope *rope, int3
     const saw::DecodeArgs d = decode_args(cache, num_q_heads, q_rot, kv_pages, scales, block_table,
                                           max_blocks_per_seq, seq_lens, num_seqs, sm_scale, out, workspace,
                                           workspace_bytes, dev_status);
-    return saw::launch_paged_decode(d, static_cast<cudaStream_t>(stream), true) == cudaSuccess ? SAW_OK
-                                                                                               : SAW_ERR_CUDA;
+    return cuda_status(saw::launch_paged_decode(d, static_cast<cudaStream_t>(stream), true));
 }
 
 int saw_decode_step_rope_mass(const saw_cache_desc *cache, const saw_rope *rope, int32_t num_q_heads,

@@ -551,3 +551,21 @@ def test_slots_past_the_ends_are_never_read_into_results(cuda_device, bits):
         for x, y in zip(*results):
             same, finite = torch.equal(x, y), bool(torch.isfinite(y.float()).all())
             assert same and finite, f"{hq}/{hkv}/{d}"
+
+
+def test_a_refused_batch_leaves_the_next_call_alone(cuda_device):
+    """More sequences than the plan's tables hold in shared memory: an error, and the next call is right."""
+    from bit_paged_kv_block_b200 import saw
+    for allocate in (lambda n: saw.allocate_mass_workspace(1, 2, n, 1, cuda_device),
+                     lambda n: saw.allocate_prefix_workspace(1, 2, n, 16, cuda_device)):
+        with pytest.raises(saw.SawError):
+            allocate(20000)
+        wl, pages, scales, q, mass = _case([20, 5], 2, 1, 128, seed=93)
+        out, got = _decode(saw, cuda_device, wl, pages, scales, q, mass, [20, 5])
+        parts = [[(wl.block_table[s], n)] for s, n in enumerate([20, 5])]
+        want, weights, terms = serving.decode_rows_fp64(u16(q), pages, scales, parts)
+        assert_bf16_close(out, want, "after a refusal")
+        _assert_mass(got, mass, wl, [20, 5], weights, terms, 128)
+        table = torch.zeros(8, 64, device=cuda_device)
+        saw.saw_rope_table(table, saw.rope_scaling())
+        assert bool((table[0, :32] == 1).all())
